@@ -221,7 +221,7 @@ def _run_own(s):
 
 def _quantize(x):
     """Codes as fp32 whole numbers, and the scales: s = amax / 127, q = x / s to the nearest, halves away from zero."""
-    s = x.abs().amax(-1) / 127
+    s = (x.abs().amax(-1).double() / 127).float()
     r = x.double() / torch.where(s > 0, s, 1.0).double()[..., None]
     return (torch.sign(r) * torch.floor(r.abs() + 0.5)).float(), s
 
@@ -309,7 +309,7 @@ def exact(case, seed):
 
     def codes(v):
         """What the codes of 64-bit rows stand for; the scale is the fp32 number that is stored."""
-        scale = (v.abs().max(dim=1).values.float() / 127).double().unsqueeze(1)
+        scale = (v.abs().max(dim=1).values.float().double() / 127).float().double().unsqueeze(1)
         scale = torch.where(scale == 0, torch.ones_like(scale), scale)
         whole = torch.trunc(v / scale)
         up = ((v / scale - whole).abs() >= 0.5).double() * torch.sign(v)
