@@ -1,0 +1,444 @@
+// elq_ops.cu -- the C ABI declared in include/elq_ops.h: host-side validation,
+// the choice of kernel, tensor maps and launches.  No allocation, no
+// synchronisation (except elq_ops_status, which is documented as blocking).
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+#include <mutex>
+#include <type_traits>
+
+#include "../../include/elq_ops.h"
+#include "ops_mma.cuh"
+
+using namespace elqops;
+
+namespace {
+
+constexpr int kMaxDevices = 64;
+constexpr int kMaxK = 65536;            // 65536 * 128 * 128 = 2^30: the int32 sum cannot overflow
+constexpr int kMaxExperts = 1024;
+
+inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+inline elq_status status_of(cudaError_t e) { return e == cudaSuccess ? ELQ_OK : ELQ_ERR_CUDA; }
+inline bool float_type(int32_t t) { return t == ELQ_F32 || t == ELQ_BF16 || t == ELQ_F16; }
+inline int type_bytes(int32_t t) { return t == ELQ_F32 ? 4 : t == ELQ_I8 ? 1 : 2; }
+
+int device_sms() {
+    static int cache[kMaxDevices] = {0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 148;
+    if (!cache[dev]) {
+        int n = 0;
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 148;
+        cache[dev] = n;
+    }
+    return cache[dev];
+}
+
+template <typename Args>
+cudaError_t launch(void (*kern)(Args), dim3 grid, int threads, size_t smem, cudaStream_t s, const Args& a) {
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
+// ---- row kernels -----------------------------------------------------------------
+
+template <int OP, bool VEC>
+cudaError_t launch_rows_v(const RowArgs& a, cudaStream_t s) {
+    const int chunks = (a.cols + 7) / 8;
+    // Chunks a thread holds: one while the row fits 512 threads, more for
+    // wider rows; from two rows per SM on, two chunks a thread (fewer warps to
+    // meet at each reduction, more rows in flight on an SM).
+    const bool many = a.rows > 2ll * device_sms();
+    int vpt = chunks <= kRowThreads ? 1 : chunks <= 2 * kRowThreads ? 2 : chunks <= 4 * kRowThreads ? 4 : 0;
+    if (many && vpt == 1 && chunks > 64) vpt = 2;
+    else if (many && vpt == 2) vpt = 4;
+    const int threads = vpt == 0 ? kRowThreads : std::max(32, ((chunks + vpt - 1) / vpt + 31) / 32 * 32);
+    const int64_t most = (int64_t)device_sms() * std::max(1, 2048 / threads);
+    const dim3 grid((unsigned)std::min<int64_t>(a.rows, most));
+    if (vpt == 1) return launch(k_rows<OP, 1, VEC>, grid, threads, 0, s, a);
+    if (vpt == 2) return launch(k_rows<OP, 2, VEC>, grid, threads, 0, s, a);
+    if (vpt == 4) return launch(k_rows<OP, 4, VEC>, grid, threads, 0, s, a);
+    return launch(k_rows<OP, 0, VEC>, grid, threads, 0, s, a);
+}
+
+// Whether rows `ld` elements of type t apart keep 16-byte alignment.
+inline bool wide(const void* p, int64_t ld, int32_t t) {
+    return !p || (aligned(p, 16) && (ld * type_bytes(t)) % 16 == 0);
+}
+
+template <int OP>
+elq_status launch_rows(const RowArgs& a, void* stream) {
+    bool vec = wide(a.x, a.ldx, a.x_type) && wide(a.h, a.ldh, a.h_type) && wide(a.h_out, a.ld_out, a.h_type) &&
+               wide(a.n, a.ldn, a.n_type) && wide(a.w, 0, ELQ_F32) && wide(a.w_next, 0, ELQ_F32);
+    if (a.gate && a.gate_cols > 1) vec = vec && wide(a.gate, a.gate_ld, ELQ_F32);
+    if (OP == ROW_SWIGLU) vec = vec && a.cols % 8 == 0;     // the up half starts on a vector
+    cudaStream_t s = (cudaStream_t)stream;
+    return status_of(vec ? launch_rows_v<OP, true>(a, s) : launch_rows_v<OP, false>(a, s));
+}
+
+// The codes a row call writes.
+elq_status check_codes(const int8_t* q, int64_t ldq, const float* scale, int64_t rows, int32_t cols) {
+    if (ldq < cols) return ELQ_ERR_INVALID_ARG;
+    if (ldq % 16) return ELQ_ERR_ALIGNMENT;
+    if (rows == 0) return ELQ_OK;
+    if (!q || !scale) return ELQ_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(scale, 4)) return ELQ_ERR_ALIGNMENT;
+    return ELQ_OK;
+}
+
+// ---- products --------------------------------------------------------------------
+
+PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, []() {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    });
+    return fn;
+}
+
+bool encode(CUtensorMap* m, int es, int rank, const void* base, const cuuint64_t* dims, const cuuint64_t* strides,
+            const cuuint32_t* box) {
+    PFN_cuTensorMapEncodeTiled_v12000 fn = map_encoder();
+    if (!fn) return false;
+    const cuuint32_t one[3] = {1, 1, 1};
+    return fn(m, es == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, rank,
+              const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Product {
+    const void* x;
+    int64_t ldx;                // elements
+    const float* sx;
+    int M;
+    const void* w;
+    int64_t ldw, w_stride;
+    const float *sw, *bias;
+    int E, N, K;
+    const int32_t* offsets;
+    void* y;
+    int y_type;
+    int64_t ldy;
+    int kind;
+};
+
+constexpr int kGemvMaxRows = 8;
+
+template <int KIND>
+cudaError_t launch_gemv(const Product& p, cudaStream_t s) {
+    constexpr int R = 2;
+    const int es = KIND == KIND_I8 ? 1 : 2;
+    GemvArgs a;
+    a.x = (const uint8_t*)p.x;
+    a.ldx = p.ldx * es;
+    a.sx = p.sx;
+    a.w = (const uint8_t*)p.w;
+    a.ldw = p.ldw * es;
+    a.w_stride = p.w_stride * es;
+    a.sw = p.sw;
+    a.bias = p.bias;
+    a.M = p.M;
+    a.E = p.E;
+    a.N = p.N;
+    a.Kb = p.K * es;
+    a.offsets = p.offsets;
+    a.y = p.y;
+    a.y_type = p.y_type;
+    a.ldy = p.ldy;
+    const int per = kGemvWarps * R;
+    const dim3 grid((unsigned)(((int64_t)p.N + per - 1) / per), p.offsets ? std::min(p.E, p.M) : 1);
+    return launch(k_gemv<KIND, R>, grid, 32 * kGemvWarps, 0, s, a);
+}
+
+template <int KIND>
+elq_status launch_mma(const Product& p, cudaStream_t s) {
+    const int es = KIND == KIND_I8 ? 1 : 2;
+    const int sms = device_sms(), ch_tiles = (int)(((int64_t)p.N + kTileCh - 1) / kTileCh);
+    MmaArgs a;
+    const cuuint64_t dw[3] = {(cuuint64_t)p.K, (cuuint64_t)p.N, (cuuint64_t)p.E};
+    const cuuint64_t sw[2] = {(cuuint64_t)(p.ldw * es), (cuuint64_t)((p.E > 1 ? p.w_stride : p.ldw * p.N) * es)};
+    const cuuint32_t bw[3] = {(cuuint32_t)(kStepBytes / es), kTileCh, 1};
+    const cuuint64_t dx[2] = {(cuuint64_t)p.K, (cuuint64_t)p.M};
+    const cuuint64_t sx[1] = {(cuuint64_t)(p.ldx * es)};
+    const cuuint32_t bx[2] = {(cuuint32_t)(kStepBytes / es), kBoxRows};
+    if (!encode(&a.tw, es, 3, p.w, dw, sw, bw) || !encode(&a.tx, es, 2, p.x, dx, sx, bx)) return ELQ_ERR_CUDA;
+    a.offsets = p.offsets;
+    a.M = p.M;
+    a.E = p.E;
+    a.N = p.N;
+    a.Kb = p.K * es;
+    a.bn = std::min(256, (p.M + 31) / 32 * 32);
+    if (!p.offsets && p.M > 32) {
+        // the row tile that takes the fewest steps: waves of tiles, each as
+        // long as its MMAs (or, below 128 rows, as its weight tile takes)
+        int64_t best = INT64_MAX;
+        for (int bn = 256; bn >= 64; bn -= 32) {
+            const int64_t tiles = ((p.M + bn - 1) / bn) * (int64_t)ch_tiles;
+            const int64_t cost = (tiles + sms - 1) / sms * (std::max(bn, 128) + 16);
+            if (cost < best) {
+                best = cost;
+                a.bn = bn;
+            }
+        }
+        a.bn = std::min(a.bn, (p.M + 31) / 32 * 32);
+    }
+    const int64_t units = ((int64_t)p.M / a.bn + p.E + 1) * ch_tiles;
+    if (units > INT32_MAX) return ELQ_ERR_UNSUPPORTED;
+    const int hdr = kMmaHdr + 2 * (p.E + 1) * 4 + 1024, stage = kABytes + a.bn * kStepBytes;
+    a.stages = std::min(kMmaStagesMax, (kMmaSmemMax - hdr) / stage);
+    a.idesc = mma_idesc(KIND);
+    a.sx = p.sx;
+    a.sw = p.sw;
+    a.bias = p.bias;
+    a.y = p.y;
+    a.y_type = p.y_type;
+    a.ldy = p.ldy;
+    static bool optin[kMaxDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return ELQ_ERR_CUDA;
+    if (dev < 0 || dev >= kMaxDevices || !optin[dev]) {
+        if (cudaFuncSetAttribute(k_mma<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMmaSmemMax) != cudaSuccess)
+            return ELQ_ERR_CUDA;
+        if (dev >= 0 && dev < kMaxDevices) optin[dev] = true;
+    }
+    return status_of(launch(k_mma<KIND>, dim3((unsigned)std::min<int64_t>(sms, units)), kMmaThreads,
+                            (size_t)(hdr + a.stages * stage), s, a));
+}
+
+elq_status run_product(const Product& p, cudaStream_t s) {
+    if (p.M <= kGemvMaxRows) {
+        return status_of(p.kind == KIND_I8     ? launch_gemv<KIND_I8>(p, s)
+                         : p.kind == KIND_BF16 ? launch_gemv<KIND_BF16>(p, s)
+                                               : launch_gemv<KIND_F16>(p, s));
+    }
+    return p.kind == KIND_I8 ? launch_mma<KIND_I8>(p, s) : p.kind == KIND_BF16 ? launch_mma<KIND_BF16>(p, s)
+                                                                               : launch_mma<KIND_F16>(p, s);
+}
+
+}  // namespace
+
+extern "C" {
+
+elq_status elq_quantize_i8(const void* x, int32_t x_type, int64_t x_rows, int32_t cols, int64_t ldx,
+                           const int32_t* index, int32_t div, int64_t rows, int8_t* q, int64_t ldq, float* scale,
+                           void* stream) {
+    if (rows < 0 || x_rows < 0 || cols < 1 || ldx < cols || div < 1) return ELQ_ERR_INVALID_ARG;
+    if (!index && rows > 0 && (div != 1 || rows > x_rows)) return ELQ_ERR_INVALID_ARG;
+    if (!float_type(x_type)) return ELQ_ERR_UNSUPPORTED;
+    const elq_status st = check_codes(q, ldq, scale, rows, cols);
+    if (st != ELQ_OK || rows == 0) return st;
+    if (!x && x_rows > 0) return ELQ_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(index, 4)) return ELQ_ERR_ALIGNMENT;
+    RowArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.rows = rows;
+    a.cols = cols;
+    a.x = x;
+    a.x_type = x_type;
+    a.ldx = ldx;
+    a.x_rows = x_rows;
+    a.index = index;
+    a.div = div;
+    a.n = q;
+    a.n_type = ELQ_I8;
+    a.ldn = ldq;
+    a.scale = scale;
+    return launch_rows<ROW_QUANT>(a, stream);
+}
+
+elq_status elq_swiglu_i8(const void* gu, int32_t x_type, int64_t rows, int32_t I, int64_t ld, int8_t* q, int64_t ldq,
+                         float* scale, void* stream) {
+    if (rows < 0 || I < 1 || I > INT32_MAX / 2 || ld < 2ll * I) return ELQ_ERR_INVALID_ARG;
+    if (!float_type(x_type)) return ELQ_ERR_UNSUPPORTED;
+    const elq_status st = check_codes(q, ldq, scale, rows, I);
+    if (st != ELQ_OK || rows == 0) return st;
+    if (!gu) return ELQ_ERR_INVALID_ARG;
+    if (!aligned(gu, 16)) return ELQ_ERR_ALIGNMENT;
+    RowArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.rows = rows;
+    a.cols = I;
+    a.x = gu;
+    a.x_type = x_type;
+    a.ldx = ld;
+    a.n = q;
+    a.n_type = ELQ_I8;
+    a.ldn = ldq;
+    a.scale = scale;
+    return launch_rows<ROW_SWIGLU>(a, stream);
+}
+
+elq_status elq_combine_i8(const void* o, int32_t o_type, int64_t o_rows, int32_t cols, int64_t ldo, const int32_t* pos,
+                          const float* weights, int64_t T, int32_t k, int8_t* q, int64_t ldq, float* scale,
+                          void* stream) {
+    if (T < 0 || o_rows < 0 || cols < 1 || ldo < cols || k < 1 || k > 64) return ELQ_ERR_INVALID_ARG;
+    if (!float_type(o_type)) return ELQ_ERR_UNSUPPORTED;
+    const elq_status st = check_codes(q, ldq, scale, T, cols);
+    if (st != ELQ_OK || T == 0) return st;
+    if ((!o && o_rows > 0) || !pos || !weights) return ELQ_ERR_INVALID_ARG;
+    if (!aligned(o, 16) || !aligned(pos, 4) || !aligned(weights, 4)) return ELQ_ERR_ALIGNMENT;
+    RowArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.rows = T;
+    a.cols = cols;
+    a.x = o;
+    a.x_type = o_type;
+    a.ldx = ldo;
+    a.x_rows = o_rows;
+    a.index = pos;
+    a.weights = weights;
+    a.k = k;
+    a.n = q;
+    a.n_type = ELQ_I8;
+    a.ldn = ldq;
+    a.scale = scale;
+    return launch_rows<ROW_COMBINE>(a, stream);
+}
+
+elq_status elq_i8_matmul(const int8_t* x, int64_t ldx, const float* sx, int64_t T, const int8_t* w, int64_t ldw,
+                         const float* sw, const float* bias, int32_t N, int32_t K, void* y, int32_t y_type, int64_t ldy,
+                         void* stream) {
+    if (T < 0 || T > INT32_MAX || N < 1 || K < 1 || ldx < K || ldw < K || ldy < N) return ELQ_ERR_INVALID_ARG;
+    if (!float_type(y_type) || K > kMaxK) return ELQ_ERR_UNSUPPORTED;
+    if (ldx % 16 || ldw % 16) return ELQ_ERR_ALIGNMENT;
+    if (T == 0) return ELQ_OK;
+    if (!x || !sx || !w || !sw || !y) return ELQ_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(w, 16) || !aligned(y, 16) || !aligned(sx, 4) || !aligned(sw, 4) ||
+        !aligned(bias, 4))
+        return ELQ_ERR_ALIGNMENT;
+    const Product p = {x, ldx, sx, (int)T, w, ldw, 0, sw, bias, 1, N, K, nullptr, y, y_type, ldy, KIND_I8};
+    return run_product(p, (cudaStream_t)stream);
+}
+
+elq_status elq_grouped_matmul(const void* x, int32_t x_type, int64_t ldx, const float* sx, int64_t M, const void* w,
+                              int64_t ldw, int64_t w_stride, const float* sw, int32_t E, int32_t N, int32_t K,
+                              const int32_t* offsets, void* y, int32_t y_type, int64_t ldy, void* stream) {
+    if (M < 0 || M > INT32_MAX || E < 1 || N < 1 || K < 1 || ldx < K || ldw < K || ldy < N) return ELQ_ERR_INVALID_ARG;
+    if (E > 1 && w_stride < (int64_t)(N - 1) * ldw + K) return ELQ_ERR_INVALID_ARG;
+    if (x_type != ELQ_I8 && x_type != ELQ_BF16 && x_type != ELQ_F16) return ELQ_ERR_UNSUPPORTED;
+    if (!float_type(y_type) || (x_type != ELQ_I8 && y_type != ELQ_F32 && y_type != x_type)) return ELQ_ERR_UNSUPPORTED;
+    if (K > kMaxK || E > kMaxExperts) return ELQ_ERR_UNSUPPORTED;
+    const int es = type_bytes(x_type);
+    if ((ldx * es) % 16 || (ldw * es) % 16 || (E > 1 && (w_stride * es) % 16)) return ELQ_ERR_ALIGNMENT;
+    if (M == 0) return ELQ_OK;
+    if (!x || !w || !offsets || !y) return ELQ_ERR_INVALID_ARG;
+    if ((x_type == ELQ_I8) != (sx != nullptr) || (x_type == ELQ_I8) != (sw != nullptr)) return ELQ_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(w, 16) || !aligned(y, 16) || !aligned(sx, 4) || !aligned(sw, 4) ||
+        !aligned(offsets, 4))
+        return ELQ_ERR_ALIGNMENT;
+    const Product p = {x, ldx, sx, (int)M, w, ldw, w_stride, sw, nullptr, E, N, K, offsets, y, y_type, ldy,
+                       x_type == ELQ_I8 ? KIND_I8 : x_type == ELQ_BF16 ? KIND_BF16 : KIND_F16};
+    return run_product(p, (cudaStream_t)stream);
+}
+
+elq_status elq_rms_norm(const void* x, int32_t x_type, int64_t T, int32_t cols, int64_t ldx, const float* weight,
+                        float eps, void* n, int32_t n_type, int64_t ldn, float* scale, void* stream) {
+    if (T < 0 || cols < 1 || ldx < cols || ldn < cols || !(eps > 0.0f) || !std::isfinite(eps))
+        return ELQ_ERR_INVALID_ARG;
+    if (!float_type(x_type) || (!float_type(n_type) && n_type != ELQ_I8)) return ELQ_ERR_UNSUPPORTED;
+    if (n_type == ELQ_I8) {
+        const elq_status st = check_codes((const int8_t*)n, ldn, scale, T, cols);
+        if (st != ELQ_OK) return st;
+    } else if (scale) {
+        return ELQ_ERR_INVALID_ARG;
+    }
+    if (T == 0) return ELQ_OK;
+    if (!x || !n) return ELQ_ERR_INVALID_ARG;
+    if (n == x && (n_type != x_type || ldn != ldx)) return ELQ_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(n, 16) || !aligned(weight, 4)) return ELQ_ERR_ALIGNMENT;
+    RowArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.rows = T;
+    a.cols = cols;
+    a.x = x;
+    a.x_type = x_type;
+    a.ldx = ldx;
+    a.w = weight;
+    a.eps = eps;
+    a.n = n;
+    a.n_type = n_type;
+    a.ldn = ldn;
+    a.scale = scale;
+    return launch_rows<ROW_RMS>(a, stream);
+}
+
+elq_status elq_residual_norm(const elq_residual* r, void* stream) {
+    if (!r) return ELQ_ERR_INVALID_ARG;
+    if (r->T < 0 || r->cols < 1 || r->ldh < r->cols || r->ldy < r->cols || r->ld_out < r->cols)
+        return ELQ_ERR_INVALID_ARG;
+    if (!(r->eps > 0.0f) || !std::isfinite(r->eps)) return ELQ_ERR_INVALID_ARG;
+    if (!float_type(r->h_type) || !float_type(r->y_type)) return ELQ_ERR_UNSUPPORTED;
+    const bool next = r->n != nullptr;
+    if (next) {
+        if (!float_type(r->n_type) && r->n_type != ELQ_I8) return ELQ_ERR_UNSUPPORTED;
+        if (r->ldn < r->cols) return ELQ_ERR_INVALID_ARG;
+        if (r->n_type == ELQ_I8) {
+            const elq_status st = check_codes((const int8_t*)r->n, r->ldn, r->scale, r->T, r->cols);
+            if (st != ELQ_OK) return st;
+        }
+    }
+    if (r->scale && !(next && r->n_type == ELQ_I8) && r->T > 0) return ELQ_ERR_INVALID_ARG;
+    if (r->gate && (r->gate_rows < 1 || (r->gate_cols != 1 && r->gate_cols != r->cols) || r->gate_ld < r->gate_cols))
+        return ELQ_ERR_INVALID_ARG;
+    if (r->T == 0) return ELQ_OK;
+    if (!r->h || !r->y || !r->h_out) return ELQ_ERR_INVALID_ARG;
+    if (r->h_out == r->h && r->ld_out != r->ldh) return ELQ_ERR_INVALID_ARG;
+    if (r->h_out == r->y || (next && (r->n == r->h || r->n == r->y || r->n == r->h_out))) return ELQ_ERR_INVALID_ARG;
+    if (!aligned(r->h, 16) || !aligned(r->y, 16) || !aligned(r->h_out, 16) || !aligned(r->n, 16) ||
+        !aligned(r->post_weight, 4) || !aligned(r->gate, 4) || !aligned(r->next_weight, 4))
+        return ELQ_ERR_ALIGNMENT;
+    RowArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.rows = r->T;
+    a.cols = r->cols;
+    a.x = r->y;
+    a.x_type = r->y_type;
+    a.ldx = r->ldy;
+    a.h = r->h;
+    a.ldh = r->ldh;
+    a.h_type = r->h_type;
+    a.h_out = r->h_out;
+    a.ld_out = r->ld_out;
+    a.w = r->post_weight;
+    a.gate = r->gate;
+    a.gate_rows = r->gate_rows;
+    a.gate_ld = r->gate_ld;
+    a.gate_cols = r->gate_cols == r->cols ? r->cols : 1;
+    a.w_next = r->next_weight;
+    a.res_scale = r->res_scale;
+    a.eps = r->eps;
+    a.n = r->n;
+    a.n_type = next ? r->n_type : ELQ_F32;
+    a.ldn = r->ldn;
+    a.scale = r->scale;
+    return launch_rows<ROW_RESIDUAL>(a, stream);
+}
+
+elq_status elq_ops_status(void* stream) {
+    if (cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess) return ELQ_ERR_CUDA;
+    int err = 0;
+    if (cudaMemcpyFromSymbol(&err, g_ops_err, sizeof(err)) != cudaSuccess) return ELQ_ERR_CUDA;
+    if (!err) return ELQ_OK;
+    const int zero = 0;
+    if (cudaMemcpyToSymbol(g_ops_err, &zero, sizeof(zero)) != cudaSuccess) return ELQ_ERR_CUDA;
+    return ELQ_ERR_TIMEOUT;
+}
+
+}  // extern "C"

@@ -1,0 +1,366 @@
+// ops_mma.cuh -- products on the 5th-generation tensor cores: dense or grouped
+// by expert with ragged sizes, 8-bit codes (kind::i8, int32 accumulators) or
+// bf16 / fp16 (kind::f16, fp32 accumulators).
+//
+// The weights are the MMA's M operand (128 channels a tile) and the rows of
+// activations its N operand, so that a ragged group costs its rows rounded up
+// to 16, not to 128, and each weight tile is read from HBM once for up to 256
+// rows.  One persistent CTA per SM; units are (expert, channel tile, row tile),
+// row tiles innermost, and CTA b takes units b, b + grid, ..., so that the CTAs
+// read neighbouring weights and the row tiles of one weight tile share it in L2.
+//
+// Warp 0 issues tensor-map copies (both operands in 128-byte K steps, 128-byte
+// swizzle) into a ring of stages, warp 1 issues the MMAs into one of two TMEM
+// accumulators, warps 4..11 drain the other: a warp reads the 32 TMEM lanes
+// (channels) it may, 32 rows at a time, rescales, and writes.  Rows of a copied
+// box that belong to the next group, or lie past the matrix (zeros), only meet
+// accumulator columns that are not written.
+#pragma once
+
+#include <cuda.h>
+
+#include "../csrc/elq_device.cuh"
+#include "ops_gemv.cuh"
+
+namespace elqops {
+
+using elq::fence_barrier_init;
+using elq::global_timer_ns;
+using elq::mbar_arrive_expect_tx;
+using elq::mbar_init;
+using elq::mbar_try_wait;
+using elq::mbar_try_wait_hint;
+using elq::smem_addr;
+
+// Set by a product whose bounded wait ran out; read and cleared by
+// elq_ops_status.
+__device__ int g_ops_err;
+
+constexpr uint64_t kOpsWaitNs = 2000000000ull;     // 2 s per bounded device wait
+constexpr int kMmaThreads = 384;
+constexpr int kMmaEpiWarps = 8;
+constexpr int kMmaStagesMax = 16;
+constexpr int kTileCh = 128;                        // channels of a tile
+constexpr int kStepBytes = 128;                     // bytes of K a stage holds
+constexpr int kABytes = kTileCh * kStepBytes;
+constexpr int kBoxRows = 32;                        // rows of one activation copy
+constexpr int kBoxBytes = kBoxRows * kStepBytes;
+constexpr int kMmaHdr = 512 + kMmaEpiWarps * 32 * 4;
+constexpr int kMmaSmemMax = 227 * 1024;
+
+struct alignas(64) MmaArgs {
+    CUtensorMap tw;             // weights [E][N][K], box 128 bytes x 128 channels
+    CUtensorMap tx;             // activations [M][K], box 128 bytes x 32 rows
+    const int32_t* offsets;     // NULL: one group of all M rows
+    int M, E, N, Kb;
+    int bn;                     // most rows of a tile: a multiple of 32, <= 256
+    int stages;
+    uint32_t idesc;             // instruction descriptor without its N field
+    const float* sx;
+    const float* sw;
+    const float* bias;
+    void* y;
+    int y_type;
+    int64_t ldy;
+};
+
+// ---- tcgen05 primitives --------------------------------------------------------
+
+__device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t cols) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(dst)), "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+template <int KIND>
+__device__ __forceinline__ void umma(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t acc) {
+    if constexpr (KIND == KIND_I8)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(ad), "l"(bd), "r"(idesc), "r"(acc)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(ad), "l"(bd), "r"(idesc), "r"(acc)
+            : "memory");
+}
+__device__ __forceinline__ void umma_commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+__device__ __forceinline__ void copy_2d(void* dst, const CUtensorMap* m, int c0, int c1, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+        "[%4];" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(smem_addr(bar))
+        : "memory");
+}
+__device__ __forceinline__ void copy_3d(void* dst, const CUtensorMap* m, int c0, int c1, int c2, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_addr(bar))
+        : "memory");
+}
+
+// 32 consecutive 32-bit TMEM columns of this thread's lane.
+__device__ __forceinline__ void tmem_read32(uint32_t t, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(t)
+        : "memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// Shared-memory descriptor of a K-major operand in 128-byte swizzled rows
+// (1024-byte groups of eight rows, one after another).
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t addr) {
+    return (uint64_t)((addr >> 4) & 0x3fff) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// Instruction descriptor without N: M = 128, both operands K-major.
+__host__ __device__ constexpr uint32_t mma_idesc(int kind) {
+    return ((uint32_t)(kTileCh >> 4) << 24) |
+           (kind == KIND_I8 ? (2u << 4) | (1u << 7) | (1u << 10)
+                            : (1u << 4) | (kind == KIND_BF16 ? (1u << 7) | (1u << 10) : 0u));
+}
+
+// Bounded wait for an mbarrier phase; gives up at once when another role has.
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatile int* abort_v) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    for (uint32_t i = 0; i < (1u << 26); ++i) {
+        if (mbar_try_wait_hint(bar, parity, 20000u)) return true;
+        if (*abort_v) return false;
+        if ((i & 15) == 15 && global_timer_ns() - t0 > kOpsWaitNs) break;
+    }
+    *abort_v = 1;
+    atomicExch(&g_ops_err, 1);
+    return false;
+}
+
+// ---- units -----------------------------------------------------------------------
+
+struct Unit {
+    int e, ch0, row0, rows, n;      // expert, first channel, first row, rows, the MMA's N
+};
+
+// s_off: the clamped offsets; s_tile[e]: row tiles of the experts before e.
+__device__ __forceinline__ Unit unit_of(int u, const int* s_off, const int* s_tile, int E, int ch_tiles) {
+    const int b = u / ch_tiles;
+    int lo = 0, hi = E;             // the last e with s_tile[e] <= b
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s_tile[mid] <= b) lo = mid;
+        else hi = mid;
+    }
+    const int nt = s_tile[lo + 1] - s_tile[lo], r = u - s_tile[lo] * ch_tiles;
+    const int ct = r / nt, t = r - ct * nt, cnt = s_off[lo + 1] - s_off[lo];
+    const int bn = ((cnt + nt - 1) / nt + 15) & ~15;        // the group's rows in nt even tiles
+    Unit x;
+    x.e = lo;
+    x.ch0 = ct * kTileCh;
+    x.row0 = s_off[lo] + t * bn;
+    x.rows = min(bn, cnt - t * bn);
+    x.n = (x.rows + 15) & ~15;
+    return x;
+}
+
+template <int KIND>
+__global__ void __launch_bounds__(kMmaThreads, 1) k_mma(const __grid_constant__ MmaArgs a) {
+    extern __shared__ uint8_t smem[];
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem);
+    uint64_t* empty = full + kMmaStagesMax;
+    uint64_t* tfull = empty + kMmaStagesMax;
+    uint64_t* tempty = tfull + 2;
+    uint64_t* drain = tempty + 2;
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drain + 1);
+    volatile int* abort_v = reinterpret_cast<volatile int*>(s_tmem + 1);
+    float* s_sx = reinterpret_cast<float*>(smem + 512);
+    int* s_off = reinterpret_cast<int*>(smem + kMmaHdr);
+    int* s_tile = s_off + a.E + 1;
+    const uint32_t tiles0 = (smem_addr(s_tile + a.E + 1) + 1023u) & ~1023u;
+    uint8_t* ring = smem + (tiles0 - smem_addr(smem));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kMmaStagesMax; ++i) {
+            mbar_init(full + i, 1);
+            mbar_init(empty + i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(tfull + i, 1);
+            mbar_init(tempty + i, kMmaEpiWarps);
+        }
+        mbar_init(drain, 1);
+        *abort_v = 0;
+        fence_barrier_init();
+    }
+    if (warp == 2) tmem_alloc(s_tmem, 512);
+    for (int i = threadIdx.x; i <= a.E; i += kMmaThreads)
+        s_off[i] = a.offsets ? clamp_offset(__ldg(a.offsets + i), a.M) : (i ? a.M : 0);
+    __syncthreads();
+    if (warp == 0) {
+        int before = 0;
+        for (int e0 = 0; e0 < a.E; e0 += 32) {
+            const int e = e0 + lane;
+            const int c = e < a.E ? max(0, s_off[e + 1] - s_off[e]) : 0;
+            int t = (c + a.bn - 1) / a.bn, s = t;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, s, o);
+                if (lane >= o) s += v;
+            }
+            if (e < a.E) s_tile[e] = before + s - t;
+            before += __shfl_sync(0xffffffffu, s, 31);
+        }
+        if (lane == 0) s_tile[a.E] = before;
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    const uint32_t tmem = *s_tmem;
+    const int ch_tiles = (a.N + kTileCh - 1) / kTileCh;
+    const int units = s_tile[a.E] * ch_tiles;
+    const int steps = (a.Kb + kStepBytes - 1) / kStepBytes;
+    const int stage_bytes = kABytes + a.bn * kStepBytes;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int st = 0;
+            uint32_t ph = 0;
+            long long issued = 0;
+            bool ok = true;
+            for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+                const Unit x = unit_of(u, s_off, s_tile, a.E, ch_tiles);
+                const int boxes = (x.n + kBoxRows - 1) / kBoxRows;
+                for (int k = 0; k < steps; ++k) {
+                    if (!(ok = bar_wait(empty + st, ph ^ 1, abort_v))) break;
+                    uint8_t* p = ring + st * stage_bytes;
+                    const int c = k * (KIND == KIND_I8 ? kStepBytes : kStepBytes / 2);
+                    mbar_arrive_expect_tx(full + st, kABytes + boxes * kBoxBytes);
+                    copy_3d(p, &a.tw, c, x.ch0, x.e, full + st);
+                    for (int b = 0; b < boxes; ++b)
+                        copy_2d(p + kABytes + b * kBoxBytes, &a.tx, c, x.row0 + b * kBoxRows, full + st);
+                    ++issued;
+                    if (++st == a.stages) {
+                        st = 0;
+                        ph ^= 1;
+                    }
+                }
+            }
+            if (!ok) {
+                // let the copies in flight land before the CTA gives up its memory
+                for (int i = 0; i < a.stages && i < issued; ++i) {
+                    const long long n = issued - 1 - i;
+                    const uint64_t t0 = global_timer_ns();
+                    while (!mbar_try_wait_hint(full + n % a.stages, (uint32_t)(n / a.stages) & 1, 20000u) &&
+                           global_timer_ns() - t0 < kOpsWaitNs) {
+                    }
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            int st = 0, it = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            for (int u = blockIdx.x; ok && u < units; u += gridDim.x, ++it) {
+                const Unit x = unit_of(u, s_off, s_tile, a.E, ch_tiles);
+                const int acc = it & 1;
+                if (!(ok = bar_wait(tempty + acc, ((it >> 1) & 1) ^ 1, abort_v))) break;
+                tc_after();
+                const uint32_t idesc = a.idesc | ((uint32_t)(x.n >> 3) << 17), d = tmem + acc * 256;
+                for (int k = 0; k < steps; ++k) {
+                    if (!(ok = bar_wait(full + st, ph, abort_v))) break;
+                    tc_after();
+                    const uint32_t p = tiles0 + st * stage_bytes;
+                    const uint64_t ad = sw128_desc(p), bd = sw128_desc(p + kABytes);
+                    const int parts = min(4, (a.Kb - k * kStepBytes + 31) / 32);
+                    for (int i = 0; i < parts; ++i) umma<KIND>(d, ad + 2 * i, bd + 2 * i, idesc, k > 0 || i > 0);
+                    umma_commit(empty + st);
+                    if (++st == a.stages) {
+                        st = 0;
+                        ph ^= 1;
+                    }
+                }
+                if (ok) umma_commit(tfull + acc);
+            }
+            if (!ok) {
+                umma_commit(drain);
+                const uint64_t t0 = global_timer_ns();
+                while (!mbar_try_wait_hint(drain, 0, 20000u) && global_timer_ns() - t0 < kOpsWaitNs) {
+                }
+            }
+        }
+    } else if (warp >= 4) {
+        const int q = warp & 3, half = (warp - 4) >> 2;
+        float* sx = s_sx + (warp - 4) * 32;
+        int it = 0;
+        for (int u = blockIdx.x; u < units; u += gridDim.x, ++it) {
+            const Unit x = unit_of(u, s_off, s_tile, a.E, ch_tiles);
+            const int acc = it & 1, n = x.ch0 + q * 32 + lane;
+            float sw = 1.0f, bias = 0.0f;
+            if (KIND == KIND_I8 && n < a.N) {
+                sw = __ldg(a.sw + (int64_t)x.e * a.N + n);
+                if (a.bias) bias = __ldg(a.bias + n);
+            }
+            if (!__all_sync(0xffffffffu, bar_wait(tfull + acc, (it >> 1) & 1, abort_v))) break;
+            tc_after();
+            for (int c = half * 32; c < x.rows; c += 64) {
+                uint32_t r[32];
+                tmem_read32(tmem + acc * 256 + c + ((uint32_t)(q * 32) << 16), r);
+                const int nr = min(32, x.rows - c);
+                if (KIND == KIND_I8) {
+                    __syncwarp();
+                    if (lane < nr) sx[lane] = __ldg(a.sx + x.row0 + c + lane);
+                    __syncwarp();
+                }
+                if (n < a.N) {
+                    const int64_t at = (int64_t)(x.row0 + c) * a.ldy + n;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        if (j < nr) {
+                            float v;
+                            if (KIND == KIND_I8) {
+                                v = __fmul_rn(__fmul_rn((float)(int)r[j], sw), sx[j]);
+                                if (a.bias) v = __fadd_rn(v, bias);
+                            } else {
+                                v = __uint_as_float(r[j]);
+                            }
+                            store1(a.y, a.y_type, at + j * a.ldy, v);
+                        }
+                    }
+                }
+                __syncwarp();
+            }
+            tc_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(tempty + acc);
+        }
+    }
+    __syncwarp();
+    tc_before();
+    __syncthreads();
+    tc_after();
+    if (warp == 2) tmem_free(tmem, 512);
+}
+
+}  // namespace elqops
