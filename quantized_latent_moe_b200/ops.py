@@ -24,7 +24,9 @@ from .elq import BF16, F32, I32, I64, V, ElqError
 
 F16, I8 = 1, 24
 TYPES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16, torch.int8: I8}
-FLOATS = (torch.float32, torch.bfloat16, torch.float16)
+FLOATS = {t: TYPES[t] for t in (torch.float32, torch.bfloat16, torch.float16)}
+HALVES = {t: TYPES[t] for t in (torch.bfloat16, torch.float16)}
+CODES, GATES = {torch.int8: I8}, {torch.float32: F32}
 F = ctypes.c_float
 INVALID, UNSUPPORTED = -1, -2
 
@@ -67,12 +69,37 @@ class I8Rows:
     """Rows as 8-bit codes ``q`` (int8 [..., rows, cols], rows a multiple of 16
     bytes apart) with one fp32 ``scale`` [..., rows] each: row r stands for
     q[r] * scale[r].  Activations have one row a token, weights one a channel,
-    expert weights [E, N, K] one a channel of each expert."""
+    expert weights [E, N, K] one a channel of each expert.
 
-    __slots__ = ("q", "scale")
+    Rows that a call here made lie in one buffer, the codes, then the scales; q
+    and scale are views of it, made when asked for."""
+
+    __slots__ = ("_q", "_scale", "_buf", "_rows", "_cols", "_ld")
 
     def __init__(self, q: torch.Tensor, scale: torch.Tensor):
-        self.q, self.scale = q, scale
+        self._q, self._scale, self._buf = q, scale, None
+
+    @classmethod
+    def _new(cls, like, rows, cols):
+        """Uninitialised rows on like's device: (rows, codes' address, elements between rows, scales' address)."""
+        r = cls.__new__(cls)
+        ld = (cols + 15) & ~15
+        r._q = r._scale = None
+        r._buf, r._rows, r._cols, r._ld = like.new_empty(rows * (ld + 4), dtype=torch.int8), rows, cols, ld
+        p = r._buf.data_ptr()
+        return r, p, ld, p + rows * ld
+
+    @property
+    def q(self) -> torch.Tensor:
+        if self._q is None:
+            self._q = self._buf.as_strided((self._rows, self._cols), (self._ld, 1))
+        return self._q
+
+    @property
+    def scale(self) -> torch.Tensor:
+        if self._scale is None:
+            self._scale = self._buf[self._rows * self._ld:].view(torch.float32)
+        return self._scale
 
     @property
     def shape(self):
@@ -84,51 +111,84 @@ class I8Rows:
 
 # ---- argument checks ------------------------------------------------------------
 
-def _refuse(ok, what, status=INVALID):
-    if not ok:
-        raise ElqError(status, what)
+def _refuse(what, status=INVALID):
+    raise ElqError(status, what)
 
 
-def _matrix(t, what, dtypes, device=None, dims=2):
-    """Checks t (dims-D, one of dtypes, contiguous rows, on device) and returns the elements between rows."""
-    _refuse(isinstance(t, torch.Tensor) and t.dim() == dims, what + ": a %d-D tensor" % dims)
-    _refuse(t.dtype in dtypes, what + ": dtype %s" % t.dtype, UNSUPPORTED)
-    _refuse(t.is_cuda and (device is None or t.device == device), what + ": device")
-    cols = t.shape[-1]
-    _refuse(cols >= 1 and (cols == 1 or t.stride(-1) == 1), what + ": contiguous rows")
-    return t.stride(-2) if t.shape[-2] > 1 else (cols + 15) // 16 * 16
+def _matrix(t, what, types, dev=None):
+    """Checks t (2-D, a dtype of types, contiguous rows, on device number dev); returns its address, type, rows,
+    columns and the elements between rows."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        _refuse(what + ": a 2-D tensor")
+    ty = types.get(t.dtype)
+    if ty is None:
+        _refuse(what + ": dtype %s" % t.dtype, UNSUPPORTED)
+    at = t.get_device()
+    if at < 0 or (dev is not None and at != dev):
+        _refuse(what + ": device")
+    rows, cols = t.shape
+    ld, one = t.stride()
+    if cols < 1 or (one != 1 and cols != 1):
+        _refuse(what + ": contiguous rows")
+    return t.data_ptr(), ty, rows, cols, ld if rows > 1 else (cols + 15) & ~15
 
 
-def _vector(t, n, what, device, dtype=torch.float32):
-    """A contiguous vector of n (or None)."""
-    if t is not None:
-        _refuse(isinstance(t, torch.Tensor) and t.dtype == dtype and t.device == device and t.numel() == n
-                and t.is_contiguous(), what + ": contiguous %s of %d values on the call's device" % (dtype, n))
-        return t.data_ptr()
-    return None
+def _vector(t, n, what, dev, dtype=torch.float32):
+    """The address of a contiguous vector of n values, or None for None."""
+    if t is None:
+        return None
+    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.get_device() == dev and t.numel() == n
+            and t.is_contiguous()):
+        _refuse("%s: %d contiguous %s values on the call's device" % (what, n, dtype))
+    return t.data_ptr()
 
 
-def _i8(m, what, device, dims=2):
-    _refuse(isinstance(m, I8Rows), what + ": I8Rows")
-    ld = _matrix(m.q, what, (torch.int8,), device, dims)
-    return ld, _vector(m.scale, m.q.numel() // m.q.shape[-1], what + ".scale", m.q.device)
+def _codes(m, what, dev=None):
+    """Codes' address, elements between rows, scales' address, rows, columns and device number of 2-D I8Rows."""
+    if not isinstance(m, I8Rows):
+        _refuse(what + ": I8Rows")
+    if m._buf is not None:
+        at = m._buf.get_device()
+        if dev is not None and at != dev:
+            _refuse(what + ": device")
+        p = m._buf.data_ptr()
+        return p, m._ld, p + m._rows * m._ld, m._rows, m._cols, at
+    p, _, rows, cols, ld = _matrix(m._q, what, CODES, dev)
+    at = m._q.get_device()
+    return p, ld, _vector(m._scale, rows, what + ".scale", at), rows, cols, at
+
+
+def _experts(t, what, types, dev):
+    """Address, elements between rows and experts, and shape of a stack [E, N, K] with contiguous rows."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 3:
+        _refuse(what + ": a 3-D tensor")
+    if t.dtype not in types:
+        _refuse(what + ": dtype %s" % t.dtype, UNSUPPORTED)
+    if t.get_device() != dev:
+        _refuse(what + ": device")
+    E, N, K = t.shape
+    st, ld, one = t.stride()
+    if K < 1 or (one != 1 and K != 1):
+        _refuse(what + ": contiguous rows")
+    return t.data_ptr(), ld if N > 1 else (K + 15) & ~15, st, E, N, K
 
 
 class _On:
-    """The device and stream of a call: ``with _On(device, stream) as raw``."""
+    """The device and stream of a call: ``with _On(device number, stream) as raw``."""
 
     __slots__ = ("guard", "raw")
 
-    def __init__(self, device, stream):
+    def __init__(self, dev, stream):
         self.guard = None
         if stream is not None:
-            _refuse(stream.device == device, "stream: of another device")
+            if stream.device.index != dev:
+                _refuse("stream: of another device")
             self.guard = torch.cuda.stream(stream)
             self.raw = stream.cuda_stream
         else:
-            if device.index != torch.cuda.current_device():
-                self.guard = torch.cuda.device(device)
-            self.raw = torch.cuda.current_stream(device).cuda_stream
+            if dev != torch.cuda.current_device():
+                self.guard = torch.cuda.device(dev)
+            self.raw = torch._C._cuda_getCurrentRawStream(dev)
 
     def __enter__(self):
         if self.guard is not None:
@@ -145,20 +205,15 @@ def _ck(status, what):
         raise ElqError(status, what)
 
 
-def _new_rows(rows, cols, device):
-    """Codes with rows padded to whole 16 bytes, and scales."""
-    ld = (cols + 15) // 16 * 16
-    q = torch.empty((rows, ld), dtype=torch.int8, device=device)
-    return (q if ld == cols else q[:, :cols]), ld, torch.empty(rows, dtype=torch.float32, device=device)
-
-
-def _out(out, rows, cols, dtype, device, what):
-    """The caller's out [rows, cols], or a new one; and the elements between its rows."""
+def _out(out, like, rows, cols, dtype, dev, what):
+    """The caller's out [rows, cols], or a new one beside `like`: tensor, address, elements between its rows."""
     if out is None:
-        return torch.empty((rows, cols), dtype=dtype, device=device), cols
-    ld = _matrix(out, what, (dtype,), device)
-    _refuse(out.shape[0] == rows and out.shape[1] == cols, what + ": shape")
-    return out, ld
+        out = like.new_empty((rows, cols), dtype=dtype)
+        return out, out.data_ptr(), cols
+    p, ty, r, c, ld = _matrix(out, what, FLOATS, dev)
+    if out.dtype != dtype or r != rows or c != cols:
+        _refuse(what + ": shape or dtype")
+    return out, p, ld
 
 
 # ---- rows to codes --------------------------------------------------------------
@@ -167,51 +222,48 @@ def quantize_i8(x: torch.Tensor, index: torch.Tensor | None = None, index_div: i
     """Codes of the rows of x [rows, K] (fp32, bf16, fp16), or of the gathered
     rows index[i] // index_div (int32 [n]; elq.route_bucket's pair order with
     index_div = k).  An expert stack [E, N, K] is quantised row by row."""
-    if x.dim() == 3:
-        _refuse(index is None and x.is_contiguous(), "quantize_i8: a contiguous [E, N, K]")
-        r = quantize_i8(x.view(-1, x.shape[-1]), stream=stream)
-        ld = (x.shape[-1] + 15) // 16 * 16
-        return I8Rows(r.q.as_strided(x.shape, (x.shape[1] * ld, ld, 1)), r.scale.view(x.shape[:2]))
-    ld = _matrix(x, "quantize_i8: x", FLOATS)
-    dev = x.device
-    rows = x.shape[0]
-    ip = None
+    if isinstance(x, torch.Tensor) and x.dim() == 3:
+        if index is not None or not x.is_contiguous():
+            _refuse("quantize_i8: a contiguous [E, N, K]")
+        E, N, K = x.shape
+        r = quantize_i8(x.view(-1, K), stream=stream)
+        return I8Rows(r._buf.as_strided(x.shape, (N * r._ld, r._ld, 1)), r.scale.view(E, N))
+    p, ty, n, cols, ld = _matrix(x, "quantize_i8: x", FLOATS)
+    dev, rows, ip = x.get_device(), n, None
     if index is not None:
         rows = index.numel()
         ip = _vector(index, rows, "quantize_i8: index", dev, torch.int32)
     with _On(dev, stream) as s:
-        q, ldq, scale = _new_rows(rows, x.shape[1], dev)
-        _ck(lib().elq_quantize_i8(x.data_ptr(), TYPES[x.dtype], x.shape[0], x.shape[1], ld, ip, index_div, rows,
-                                  q.data_ptr(), ldq, scale.data_ptr(), s), "elq_quantize_i8")
-    return I8Rows(q, scale)
+        r, q, ldq, scale = I8Rows._new(x, rows, cols)
+        _ck(lib().elq_quantize_i8(p, ty, n, cols, ld, ip, index_div, rows, q, ldq, scale, s), "elq_quantize_i8")
+    return r
 
 
 def swiglu_i8(gu: torch.Tensor, stream=None) -> I8Rows:
     """Codes of silu(gate) * up for gu [rows, 2 I] = [gate | up]."""
-    ld = _matrix(gu, "swiglu_i8: gu", FLOATS)
-    _refuse(gu.shape[1] % 2 == 0, "swiglu_i8: an even number of columns")
-    rows, I = gu.shape[0], gu.shape[1] // 2
-    with _On(gu.device, stream) as s:
-        q, ldq, scale = _new_rows(rows, I, gu.device)
-        _ck(lib().elq_swiglu_i8(gu.data_ptr(), TYPES[gu.dtype], rows, I, ld, q.data_ptr(), ldq, scale.data_ptr(), s),
-            "elq_swiglu_i8")
-    return I8Rows(q, scale)
+    p, ty, rows, cols, ld = _matrix(gu, "swiglu_i8: gu", FLOATS)
+    if cols % 2:
+        _refuse("swiglu_i8: an even number of columns")
+    with _On(gu.get_device(), stream) as s:
+        r, q, ldq, scale = I8Rows._new(gu, rows, cols // 2)
+        _ck(lib().elq_swiglu_i8(p, ty, rows, cols // 2, ld, q, ldq, scale, s), "elq_swiglu_i8")
+    return r
 
 
 def combine_i8(o: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor, stream=None) -> I8Rows:
     """Codes of sum_j weights[t, j] * o[pos[t, j]]: o [rows, L], weights fp32
     [T, k], pos int32 of T * k row numbers (elq.route_bucket's pos)."""
-    ld = _matrix(o, "combine_i8: o", FLOATS)
-    dev = o.device
-    _refuse(weights.dim() == 2, "combine_i8: weights [T, k]")
+    p, ty, n, cols, ld = _matrix(o, "combine_i8: o", FLOATS)
+    dev = o.get_device()
+    if weights.dim() != 2:
+        _refuse("combine_i8: weights [T, k]")
     T, k = weights.shape
     wp = _vector(weights, T * k, "combine_i8: weights", dev)
     pp = _vector(pos, T * k, "combine_i8: pos", dev, torch.int32)
     with _On(dev, stream) as s:
-        q, ldq, scale = _new_rows(T, o.shape[1], dev)
-        _ck(lib().elq_combine_i8(o.data_ptr(), TYPES[o.dtype], o.shape[0], o.shape[1], ld, pp, wp, T, k,
-                                 q.data_ptr(), ldq, scale.data_ptr(), s), "elq_combine_i8")
-    return I8Rows(q, scale)
+        r, q, ldq, scale = I8Rows._new(o, T, cols)
+        _ck(lib().elq_combine_i8(p, ty, n, cols, ld, pp, wp, T, k, q, ldq, scale, s), "elq_combine_i8")
+    return r
 
 
 # ---- products -------------------------------------------------------------------
@@ -220,18 +272,17 @@ def i8_matmul(x: I8Rows, w: I8Rows, bias: torch.Tensor | None = None, out_dtype=
               out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """y [T, N] = x [T, K] times w [N, K] transposed, from their codes, plus bias
     (fp32 [N])."""
-    ldx, sx = _i8(x, "i8_matmul: x", None)
-    dev = x.q.device
-    ldw, sw = _i8(w, "i8_matmul: w", dev)
-    T, K = x.q.shape
-    N = w.q.shape[0]
-    _refuse(w.q.shape[1] == K, "i8_matmul: K of x and w")
-    _refuse(out_dtype in FLOATS, "i8_matmul: out_dtype", UNSUPPORTED)
+    xp, ldx, sx, T, K, dev = _codes(x, "i8_matmul: x")
+    wp, ldw, sw, N, Kw, _ = _codes(w, "i8_matmul: w", dev)
+    if K != Kw:
+        _refuse("i8_matmul: K of x and w")
+    yt = FLOATS.get(out_dtype)
+    if yt is None:
+        _refuse("i8_matmul: out_dtype", UNSUPPORTED)
     bp = _vector(bias, N, "i8_matmul: bias", dev)
     with _On(dev, stream) as s:
-        y, ldy = _out(out, T, N, out_dtype, dev, "i8_matmul: out")
-        _ck(lib().elq_i8_matmul(x.q.data_ptr(), ldx, sx, T, w.q.data_ptr(), ldw, sw, bp, N, K, y.data_ptr(),
-                                TYPES[out_dtype], ldy, s), "elq_i8_matmul")
+        y, yp, ldy = _out(out, w._q if w._buf is None else w._buf, T, N, out_dtype, dev, "i8_matmul: out")
+        _ck(lib().elq_i8_matmul(xp, ldx, sx, T, wp, ldw, sw, bp, N, K, yp, yt, ldy, s), "elq_i8_matmul")
     return y
 
 
@@ -244,26 +295,31 @@ def grouped_matmul(x, w, offsets: torch.Tensor, out_dtype=None, out: torch.Tenso
     has them (undefined without out)."""
     codes = isinstance(x, I8Rows)
     if codes:
-        ldx, sx = _i8(x, "grouped_matmul: x", None)
-        ldw, sw = _i8(w, "grouped_matmul: w", x.q.device, 3)
-        xt, wt = x.q, w.q
+        xp, ldx, sx, M, K, dev = _codes(x, "grouped_matmul: x")
+        if not isinstance(w, I8Rows):
+            _refuse("grouped_matmul: w: I8Rows")
+        xt, wt = I8, w.q
+        wp, ldw, st, E, N, Kw = _experts(wt, "grouped_matmul: w", CODES, dev)
+        sw = _vector(w.scale, E * N, "grouped_matmul: w.scale", dev)
     else:
-        ldx, sx = _matrix(x, "grouped_matmul: x", (torch.bfloat16, torch.float16)), None
-        ldw, sw = _matrix(w, "grouped_matmul: w", (x.dtype,), x.device, 3), None
-        xt, wt = x, w
-    dev = xt.device
-    M, K = xt.shape
-    E, N = wt.shape[0], wt.shape[1]
-    _refuse(wt.shape[2] == K, "grouped_matmul: K of x and w")
+        xp, xt, M, K, ldx = _matrix(x, "grouped_matmul: x", HALVES)
+        dev, wt = x.get_device(), w
+        wp, ldw, st, E, N, Kw = _experts(wt, "grouped_matmul: w", (x.dtype,), dev)
+        sx = sw = None
+    if K != Kw:
+        _refuse("grouped_matmul: K of x and w")
+    if offsets is None:
+        _refuse("grouped_matmul: offsets")
     op = _vector(offsets, E + 1, "grouped_matmul: offsets", dev, torch.int32)
-    _refuse(op is not None, "grouped_matmul: offsets")
     if out_dtype is None:
         out_dtype = out.dtype if out is not None else torch.float32 if codes else x.dtype
-    _refuse(out_dtype in FLOATS, "grouped_matmul: out_dtype", UNSUPPORTED)
+    yt = FLOATS.get(out_dtype)
+    if yt is None:
+        _refuse("grouped_matmul: out_dtype", UNSUPPORTED)
     with _On(dev, stream) as s:
-        y, ldy = _out(out, M, N, out_dtype, dev, "grouped_matmul: out")
-        _ck(lib().elq_grouped_matmul(xt.data_ptr(), TYPES[xt.dtype], ldx, sx, M, wt.data_ptr(), ldw, wt.stride(0), sw,
-                                     E, N, K, op, y.data_ptr(), TYPES[out_dtype], ldy, s), "elq_grouped_matmul")
+        y, yp, ldy = _out(out, wt, M, N, out_dtype, dev, "grouped_matmul: out")
+        _ck(lib().elq_grouped_matmul(xp, xt, ldx, sx, M, wp, ldw, st, sw, E, N, K, op, yp, yt, ldy, s),
+            "elq_grouped_matmul")
     return y
 
 
@@ -273,31 +329,29 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float = 1
              out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """x / sqrt(mean(x^2) + eps) * weight, row by row, in x's dtype or out_dtype;
     out may be x."""
-    ld = _matrix(x, "rms_norm: x", FLOATS)
-    dev = x.device
-    T, C = x.shape
+    p, ty, T, C, ld = _matrix(x, "rms_norm: x", FLOATS)
+    dev = x.get_device()
     wp = _vector(weight, C, "rms_norm: weight", dev)
     if out_dtype is None:
         out_dtype = x.dtype if out is None else out.dtype
-    _refuse(out_dtype in FLOATS, "rms_norm: out_dtype", UNSUPPORTED)
+    nt = FLOATS.get(out_dtype)
+    if nt is None:
+        _refuse("rms_norm: out_dtype", UNSUPPORTED)
     with _On(dev, stream) as s:
-        n, ldn = _out(out, T, C, out_dtype, dev, "rms_norm: out")
-        _ck(lib().elq_rms_norm(x.data_ptr(), TYPES[x.dtype], T, C, ld, wp, eps, n.data_ptr(), TYPES[out_dtype], ldn,
-                               None, s), "elq_rms_norm")
+        n, np, ldn = _out(out, x, T, C, out_dtype, dev, "rms_norm: out")
+        _ck(lib().elq_rms_norm(p, ty, T, C, ld, wp, eps, np, nt, ldn, None, s), "elq_rms_norm")
     return n
 
 
 def rms_norm_i8(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float = 1e-6, stream=None) -> I8Rows:
     """rms_norm handed straight to the row quantiser (the fp32 norm, unrounded)."""
-    ld = _matrix(x, "rms_norm_i8: x", FLOATS)
-    dev = x.device
-    T, C = x.shape
+    p, ty, T, C, ld = _matrix(x, "rms_norm_i8: x", FLOATS)
+    dev = x.get_device()
     wp = _vector(weight, C, "rms_norm_i8: weight", dev)
     with _On(dev, stream) as s:
-        q, ldq, scale = _new_rows(T, C, dev)
-        _ck(lib().elq_rms_norm(x.data_ptr(), TYPES[x.dtype], T, C, ld, wp, eps, q.data_ptr(), I8, ldq,
-                               scale.data_ptr(), s), "elq_rms_norm")
-    return I8Rows(q, scale)
+        r, q, ldq, scale = I8Rows._new(x, T, C)
+        _ck(lib().elq_rms_norm(p, ty, T, C, ld, wp, eps, q, I8, ldq, scale, s), "elq_rms_norm")
+    return r
 
 
 def residual_norm(h: torch.Tensor, y: torch.Tensor, post_weight: torch.Tensor | None = None, *,
@@ -311,41 +365,42 @@ def residual_norm(h: torch.Tensor, y: torch.Tensor, post_weight: torch.Tensor | 
     gate: fp32 [C] (a value a channel), [G, C], or [G, 1] (a value a row); row t
     takes gate row t // gate_rows, by default T for G = 1 and 1 for G = T.  out: h'
     (h itself for in-place)."""
-    ldh = _matrix(h, "residual_norm: h", FLOATS)
-    dev = h.device
-    ldy = _matrix(y, "residual_norm: y", FLOATS, dev)
-    T, C = h.shape
-    _refuse(y.shape == h.shape, "residual_norm: shapes of h and y")
-    r = ResidualC()
-    r.T, r.cols, r.h_type, r.y_type = T, C, TYPES[h.dtype], TYPES[y.dtype]
-    r.h, r.y, r.ldh, r.ldy = h.data_ptr(), y.data_ptr(), ldh, ldy
-    r.post_weight = _vector(post_weight, C, "residual_norm: post_weight", dev)
+    hp, ht, T, C, ldh = _matrix(h, "residual_norm: h", FLOATS)
+    dev = h.get_device()
+    yp, yt, Ty, Cy, ldy = _matrix(y, "residual_norm: y", FLOATS, dev)
+    if T != Ty or C != Cy:
+        _refuse("residual_norm: shapes of h and y")
+    pw = _vector(post_weight, C, "residual_norm: post_weight", dev)
+    gp, g_rows, gc, ldg = None, 1, 1, 1
     if gate is not None:
-        g = gate.unsqueeze(0) if gate.dim() == 1 else gate
-        r.gate_ld = _matrix(g, "residual_norm: gate", (torch.float32,), dev)
-        G = g.shape[0]
-        _refuse(g.shape[1] in (1, C), "residual_norm: gate columns")
-        if gate_rows is None:
-            _refuse(G == 1 or G == T, "residual_norm: gate rows")
-            gate_rows = max(T, 1) if G == 1 else 1
-        _refuse(gate_rows >= 1 and G * gate_rows >= T, "residual_norm: gate rows")
-        r.gate, r.gate_rows, r.gate_cols = g.data_ptr(), gate_rows, g.shape[1]
-    r.res_scale, r.eps = res_scale, eps
+        if gate.dim() == 1:
+            G, gc, ldg, gp = 1, gate.numel(), gate.numel(), _vector(gate, gate.numel(), "residual_norm: gate", dev)
+        else:
+            gp, _, G, gc, ldg = _matrix(gate, "residual_norm: gate", GATES, dev)
+        if gc != C and gc != 1:
+            _refuse("residual_norm: gate columns")
+        g_rows = gate_rows
+        if g_rows is None:
+            if G != 1 and G != T:
+                _refuse("residual_norm: gate rows")
+            g_rows = max(T, 1) if G == 1 else 1
+        if g_rows < 1 or G * g_rows < T:
+            _refuse("residual_norm: gate rows")
     with _On(dev, stream) as s:
-        h_out, r.ld_out = _out(out, T, C, h.dtype, dev, "residual_norm: out")
-        r.h_out = h_out.data_ptr()
-        n = None
+        h_out, op, ldo = _out(out, h, T, C, h.dtype, dev, "residual_norm: out")
+        n = nw = np = scale = None
+        nt = ldn = 0
         if next_dtype is not None:
-            r.next_weight = _vector(next_weight, C, "residual_norm: next_weight", dev)
-            if next_dtype == torch.int8:
-                q, r.ldn, scale = _new_rows(T, C, dev)
-                n = I8Rows(q, scale)
-                r.n, r.scale = q.data_ptr(), scale.data_ptr()
+            nw = _vector(next_weight, C, "residual_norm: next_weight", dev)
+            nt = TYPES.get(next_dtype)
+            if nt is None:
+                _refuse("residual_norm: next_dtype", UNSUPPORTED)
+            if nt == I8:
+                n, np, ldn, scale = I8Rows._new(h, T, C)
             else:
-                _refuse(next_dtype in FLOATS, "residual_norm: next_dtype", UNSUPPORTED)
-                n, r.ldn = _out(None, T, C, next_dtype, dev, "")
-                r.n = n.data_ptr()
-            r.n_type = TYPES[next_dtype]
+                n, np, ldn = _out(None, h, T, C, next_dtype, dev, "")
+        r = ResidualC(T, C, ht, yt, nt, hp, yp, pw, gp, nw, op, np, scale, ldh, ldy, ldo, ldn, g_rows, ldg, gc, res_scale,
+                      eps)
         _ck(lib().elq_residual_norm(ctypes.byref(r), s), "elq_residual_norm")
     return h_out, n
 
@@ -353,6 +408,6 @@ def residual_norm(h: torch.Tensor, y: torch.Tensor, post_weight: torch.Tensor | 
 def status(device=None, stream=None) -> int:
     """Blocking: whether a product's bounded device wait ran out since the last
     call (0, or the timeout status)."""
-    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    with _On(device, stream) as s:
+    dev = torch.cuda.current_device() if device is None else torch.device(device).index
+    with _On(dev, stream) as s:
         return int(lib().elq_ops_status(s))
