@@ -41,11 +41,11 @@ int device_sms() {
 }
 
 template <typename Args>
-cudaError_t launch(void (*kern)(Args), dim3 grid, int threads, size_t smem, cudaStream_t s, const Args& a) {
+cudaError_t launch(void (*kern)(Args), dim3 grid, dim3 threads, size_t smem, cudaStream_t s, const Args& a) {
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof(cfg));
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
+    cfg.blockDim = threads;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     return cudaLaunchKernelEx(&cfg, kern, a);
@@ -53,23 +53,89 @@ cudaError_t launch(void (*kern)(Args), dim3 grid, int threads, size_t smem, cuda
 
 // ---- row kernels -----------------------------------------------------------------
 
+constexpr int kPipeSmem = 200 * 1024;       // most shared memory of a k_pipe CTA
+
+template <int OP, int VPT, int D, int XT>
+cudaError_t launch_pipe_t(const RowArgs& a, int threads, int groups, size_t smem, cudaStream_t s) {
+    static bool optin[kMaxDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices || !optin[dev]) {
+        e = cudaFuncSetAttribute(k_pipe<OP, VPT, D, XT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPipeSmem);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < kMaxDevices) optin[dev] = true;
+    }
+    // as many CTAs as fit, by registers (64 a thread with one chunk, 80 with more) and by shared memory
+    const int fit = std::max(1, std::min((VPT == 1 ? 1024 : 768) / (threads * groups), (int)(224 * 1024 / (smem + 2048))));
+    const dim3 grid((unsigned)std::min<int64_t>((a.rows + groups - 1) / groups, (int64_t)device_sms() * fit));
+    return launch(k_pipe<OP, VPT, D, XT>, grid, dim3(threads, groups), smem, s, a);
+}
+
+// Rows through shared memory; false where they are too long for it.
+template <int OP>
+bool launch_pipe(RowArgs a, cudaStream_t s, cudaError_t* e) {
+    const int chunks = (a.cols + 7) / 8;
+    if (chunks > 4 * kPipeThreads4) return false;
+    // Few rows: one chunk a thread, the shortest way through a row.  Many: up to
+    // four, since a thread's work per row besides its values (reductions, the
+    // scale, addresses) is as much as two or three chunks'.
+    const bool many = a.rows > 2 * device_sms();
+    int vpt = chunks <= kRowThreads ? 1 : 4;
+    if (many && chunks > 32) vpt = 4;
+    const int threads = std::max(32, ((chunks + vpt - 1) / vpt + 31) / 32 * 32);
+    const bool gate = OP == ROW_RESIDUAL && a.gate && a.gate_cols > 1;
+    a.w_planes = OP == ROW_RMS ? 2 : OP == ROW_RESIDUAL ? 4 : 0;
+    a.row_planes = planes_of(a.x_type) * (OP == ROW_SWIGLU ? 2 : 1) + (OP == ROW_RESIDUAL ? planes_of(a.h_type) : 0) +
+                   (gate && a.gate_rows < a.rows ? 2 : 0);
+    const size_t plane = (size_t)vpt * threads * 16;
+    // Many rows with weights to share: several rows of a CTA at a time (2048 x 4096
+    // bf16, residual norm: 21.2 us with three, 27.9 with one; norm: 12.3 and 19.5).
+    int groups = 1, d = 1;
+    auto smem = [&](int g, int dd) { return (a.w_planes + (size_t)g * dd * a.row_planes) * plane; };
+    if (many) {
+        if (vpt == 4 && a.w_planes)
+            groups = std::min(kRowGroups, kPipeThreads4 / threads);
+        // three stages a row, else two, and fewer rows before fewer stages
+        while (groups > 1 && smem(groups, 2) > kPipeSmem) --groups;
+        d = smem(groups, 3) <= kPipeSmem ? 3 : smem(groups, 2) <= kPipeSmem ? 2 : 1;
+    }
+    if (smem(groups, d) > kPipeSmem) return false;
+    auto go = [&](auto v, auto dd) {
+        constexpr int V = decltype(v)::value, D = decltype(dd)::value;
+        if constexpr (OP == ROW_RESIDUAL) *e = launch_pipe_t<OP, V, D, kAnyType>(a, threads, groups, smem(groups, d), s);
+        else if (a.x_type == ELQ_F32) *e = launch_pipe_t<OP, V, D, ELQ_F32>(a, threads, groups, smem(groups, d), s);
+        else if (a.x_type == ELQ_BF16) *e = launch_pipe_t<OP, V, D, ELQ_BF16>(a, threads, groups, smem(groups, d), s);
+        else *e = launch_pipe_t<OP, V, D, ELQ_F16>(a, threads, groups, smem(groups, d), s);
+    };
+    using one = std::integral_constant<int, 1>;
+    using two = std::integral_constant<int, 2>;
+    using three = std::integral_constant<int, 3>;
+    using four = std::integral_constant<int, 4>;
+    if (vpt == 1) d == 1 ? go(one(), one()) : go(one(), three());
+    else d == 1 ? go(four(), one()) : d == 2 ? go(four(), two()) : go(four(), three());
+    return true;
+}
+
+template <int OP, int VPT, bool VEC>
+cudaError_t launch_rows_t(const RowArgs& a, int threads, cudaStream_t s) {
+    const int64_t most = (int64_t)device_sms() * std::max(1, 2048 / threads);
+    return launch(k_rows<OP, VPT, VEC>, dim3((unsigned)std::min<int64_t>(a.rows, most)), threads, 0, s, a);
+}
+
+// k_rows: chunks of a row in registers, as few a thread as 512 threads allow,
+// or none for rows past 16384 values.
 template <int OP, bool VEC>
 cudaError_t launch_rows_v(const RowArgs& a, cudaStream_t s) {
     const int chunks = (a.cols + 7) / 8;
-    // Chunks a thread holds: one while the row fits 512 threads, more for
-    // wider rows; from two rows per SM on, two chunks a thread (fewer warps to
-    // meet at each reduction, more rows in flight on an SM).
-    const bool many = a.rows > 2ll * device_sms();
-    int vpt = chunks <= kRowThreads ? 1 : chunks <= 2 * kRowThreads ? 2 : chunks <= 4 * kRowThreads ? 4 : 0;
-    if (many && vpt == 1 && chunks > 64) vpt = 2;
-    else if (many && vpt == 2) vpt = 4;
+    const int vpt = chunks <= kRowThreads ? 1 : chunks <= 2 * kRowThreads ? 2 : chunks <= 4 * kRowThreads ? 4 : 0;
     const int threads = vpt == 0 ? kRowThreads : std::max(32, ((chunks + vpt - 1) / vpt + 31) / 32 * 32);
-    const int64_t most = (int64_t)device_sms() * std::max(1, 2048 / threads);
-    const dim3 grid((unsigned)std::min<int64_t>(a.rows, most));
-    if (vpt == 1) return launch(k_rows<OP, 1, VEC>, grid, threads, 0, s, a);
-    if (vpt == 2) return launch(k_rows<OP, 2, VEC>, grid, threads, 0, s, a);
-    if (vpt == 4) return launch(k_rows<OP, 4, VEC>, grid, threads, 0, s, a);
-    return launch(k_rows<OP, 0, VEC>, grid, threads, 0, s, a);
+    if constexpr (OP == ROW_COMBINE || !VEC) {      // aligned rows of the others go through k_pipe
+        if (vpt == 1) return launch_rows_t<OP, 1, VEC>(a, threads, s);
+        if (vpt == 2) return launch_rows_t<OP, 2, VEC>(a, threads, s);
+        if (vpt == 4) return launch_rows_t<OP, 4, VEC>(a, threads, s);
+    }
+    return launch_rows_t<OP, 0, VEC>(a, kRowThreads, s);
 }
 
 // Whether rows `ld` elements of type t apart keep 16-byte alignment.
@@ -78,12 +144,17 @@ inline bool wide(const void* p, int64_t ld, int32_t t) {
 }
 
 template <int OP>
-elq_status launch_rows(const RowArgs& a, void* stream) {
+elq_status launch_rows(RowArgs a, void* stream) {
+    a.inv_cols = 1.0f / (float)a.cols;
     bool vec = wide(a.x, a.ldx, a.x_type) && wide(a.h, a.ldh, a.h_type) && wide(a.h_out, a.ld_out, a.h_type) &&
                wide(a.n, a.ldn, a.n_type) && wide(a.w, 0, ELQ_F32) && wide(a.w_next, 0, ELQ_F32);
     if (a.gate && a.gate_cols > 1) vec = vec && wide(a.gate, a.gate_ld, ELQ_F32);
     if (OP == ROW_SWIGLU) vec = vec && a.cols % 8 == 0;     // the up half starts on a vector
     cudaStream_t s = (cudaStream_t)stream;
+    if constexpr (OP != ROW_COMBINE) {
+        cudaError_t e = cudaSuccess;
+        if (vec && launch_pipe<OP>(a, s, &e)) return status_of(e);
+    }
     return status_of(vec ? launch_rows_v<OP, true>(a, s) : launch_rows_v<OP, false>(a, s));
 }
 

@@ -48,22 +48,6 @@ __device__ __forceinline__ uint4 load_tail(const uint8_t* p, int n) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <int KIND>
-__device__ __forceinline__ void widen8(const uint4& r, float (&v)[8]) {
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        if (KIND == KIND_BF16) {
-            v[2 * j] = bf16_lo(w[j]);
-            v[2 * j + 1] = bf16_hi(w[j]);
-        } else {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
-            v[2 * j] = f.x;
-            v[2 * j + 1] = f.y;
-        }
-    }
-}
-
 // Sums of C values over the warp, by halves: at each step a lane passes on the
 // half of its values that its partner keeps.  Lane l ends with the sum of value
 // l >> (5 - log2 C).
@@ -102,11 +86,11 @@ __device__ __forceinline__ void gemv_piece(const uint4 (&w)[R], const uint4 (&x)
     } else {
         float wf[R][8];
 #pragma unroll
-        for (int r = 0; r < R; ++r) widen8<KIND>(w[r], wf[r]);
+        for (int r = 0; r < R; ++r) widen8(w[r], KIND == KIND_BF16 ? ELQ_BF16 : ELQ_F16, wf[r]);
 #pragma unroll
         for (int t = 0; t < TB; ++t) {
             float xf[8];
-            widen8<KIND>(x[t], xf);
+            widen8(x[t], KIND == KIND_BF16 ? ELQ_BF16 : ELQ_F16, xf);
 #pragma unroll
             for (int r = 0; r < R; ++r)
 #pragma unroll

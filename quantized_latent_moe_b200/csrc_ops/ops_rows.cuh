@@ -2,13 +2,19 @@
 // gathered, SwiGLU'd, or a weighted sum of expert rows), and the norms before
 // and after a block.
 //
-// All are one pass over memory.  A CTA owns a row at a time (grid-strided): it
-// loads the row's inputs once into registers as fp32, takes the row's
-// reductions (sum of squares, largest magnitude) by warp shuffles and one
-// shared-memory exchange each, and writes the outputs.  What bounds them is
-// HBM traffic for many rows and launch-to-finish latency for one.  Rows longer
-// than the registers of a CTA hold (16384 values) take the same steps but read
-// their inputs again for each step.
+// All are one pass over memory: a CTA owns a row at a time (grid-strided), takes
+// the row's reductions (sum of squares, largest magnitude) by warp shuffles and
+// one shared-memory exchange each, and writes the outputs.  What bounds them is
+// HBM traffic for many rows and launch-to-finish latency for one.
+//
+//  k_pipe   rows whose pieces are 16-byte aligned, up to 12288 values: each
+//           thread copies its own pieces of the next rows into shared memory
+//           asynchronously (cp.async, no barrier needed to read them back) while
+//           it works on the current one, and the norms' weights once per CTA.
+//  k_rows   the rest: the weighted combine (its k rows a token are already that
+//           many independent loads), unaligned rows (element by element), and
+//           rows longer than a CTA's registers hold, which take the same steps
+//           but read their inputs again for each.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -39,7 +45,7 @@ struct RowArgs {
     int64_t gate_rows, gate_ld;
     int gate_cols;
     const float* w_next;
-    float res_scale, eps;
+    float res_scale, eps, inv_cols;
     // outputs
     void* h_out;
     int h_type;
@@ -48,6 +54,8 @@ struct RowArgs {
     int n_type;
     int64_t ldn;
     float* scale;
+    // k_pipe: what a CTA keeps in shared memory
+    int w_planes, row_planes;   // 16-byte pieces a thread's chunk has of the weights, and of a row
 };
 
 constexpr int kRowThreads = 512;        // most threads of a CTA
@@ -56,10 +64,24 @@ constexpr int kRowMaxCols = kRowThreads * 8 * 4;
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-__device__ __forceinline__ float load1(const void* p, int type, int64_t i) {
-    if (type == ELQ_F32) return reinterpret_cast<const float*>(p)[i];
-    const uint16_t b = reinterpret_cast<const uint16_t*>(p)[i];
-    return type == ELQ_BF16 ? __uint_as_float((uint32_t)b << 16) : __half2float(__ushort_as_half(b));
+// Eight 16-bit values.
+__device__ __forceinline__ void widen8(const uint4& r, int type, float (&v)[8]) {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+    // one branch for all eight, not a choice between two conversions of each
+    if (type == ELQ_BF16) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[2 * j] = bf16_lo(w[j]);
+            v[2 * j + 1] = bf16_hi(w[j]);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+            v[2 * j] = f.x;
+            v[2 * j + 1] = f.y;
+        }
+    }
 }
 
 // Eight consecutive values from element i (a multiple of 8 from a 16-byte
@@ -72,32 +94,19 @@ __device__ __forceinline__ void load8(const void* p, int type, int64_t i, float 
         v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
         return;
     }
-    const uint4 r = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p) + i);
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        if (type == ELQ_BF16) {
-            v[2 * j] = bf16_lo(w[j]);
-            v[2 * j + 1] = bf16_hi(w[j]);
-        } else {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
-            v[2 * j] = f.x;
-            v[2 * j + 1] = f.y;
-        }
-    }
+    widen8(*reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p) + i), type, v);
 }
-
 __device__ __forceinline__ void store1(void* p, int type, int64_t i, float v) {
     if (type == ELQ_F32) reinterpret_cast<float*>(p)[i] = v;
     else if (type == ELQ_BF16) reinterpret_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
     else reinterpret_cast<__half*>(p)[i] = __float2half_rn(v);
 }
 
-__device__ __forceinline__ uint32_t pack2(int type, float a, float b) {
-    if (type == ELQ_BF16) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-        return *reinterpret_cast<const uint32_t*>(&h);
-    }
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
     const __half2 h = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
@@ -109,134 +118,209 @@ __device__ __forceinline__ void store8(void* p, int type, int64_t i, const float
         d[1] = make_float4(v[4], v[5], v[6], v[7]);
         return;
     }
-    *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p) + i) =
-        make_uint4(pack2(type, v[0], v[1]), pack2(type, v[2], v[3]), pack2(type, v[4], v[5]), pack2(type, v[6], v[7]));
+    uint4* d = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p) + i);
+    if (type == ELQ_BF16)
+        *d = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+    else
+        *d = make_uint4(pack_f16(v[0], v[1]), pack_f16(v[2], v[3]), pack_f16(v[4], v[5]), pack_f16(v[6], v[7]));
 }
 
 // The scale of a row and what its codes need: x / s to the nearest whole
-// number, exactly.  rint(|x| * inv) is within one of it; the remainder
-// |x| - q * s is exact in fp32 (one fused multiply-add), and its comparison
-// with s / 2 settles the rounding, halves away from zero.  A scale below
-// 2^-100 is worked on times 2^100 (exact) so that its reciprocal is finite.
+// number, exactly.  q = rint(x * inv) is within one of it; the remainder
+// r = x - q * s is exact in fp32 (one fused multiply-add), and its comparison
+// with s / 2 settles the rounding, halves away from zero.  A scale below 2^-100
+// is worked on times 2^100 (exact) so that its reciprocal is finite.
 struct CodeScale {
-    float s, sm, inv, up;       // the scale, the scale and factor it is worked on with
+    float s, sm, half, inv, up;     // the scale; the scale, its half, reciprocal and factor as worked on
 };
 
-// amax_bits: the largest bit pattern of |x| over the row (an infinity or NaN
-// has the largest of all).
+// amax_bits: the bits of the row's largest magnitude (as unsigned numbers, those
+// of an infinity or NaN are the largest of all).
 __device__ __forceinline__ CodeScale code_scale(uint32_t amax_bits) {
     CodeScale c;
     if (amax_bits >= 0x7f800000u) {
         c.s = __uint_as_float(0x7fffffffu);
-        c.sm = c.inv = c.up = 0.0f;
+        c.sm = c.half = c.inv = 0.0f;
+        c.up = 1.0f;
         return c;
     }
     c.s = __fdiv_rn(__uint_as_float(amax_bits), 127.0f);
     c.up = c.s < 7.88860905e-31f ? 1.2676506e30f : 1.0f;       // 2^-100, 2^100
     c.sm = __fmul_rn(c.s, c.up);
-    c.inv = c.s > 0.0f ? __fdiv_rn(1.0f, c.sm) : 0.0f;
+    c.half = 0.5f * c.sm;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(c.inv) : "f"(c.sm));     // a first guess is all it gives
+    if (c.s == 0.0f) c.inv = 0.0f;
     return c;
+}
+
+// The code of x, given its first guess q.
+__device__ __forceinline__ float code_settle(float x, float q, const CodeScale& c) {
+    const float r = __fmaf_rn(-q, c.sm, x);
+    if (r > c.half || (r == c.half && x > 0.0f)) q += 1.0f;
+    else if (r < -c.half || (r == -c.half && x < 0.0f)) q -= 1.0f;
+    return q;
 }
 
 __device__ __forceinline__ int code_of(float x, const CodeScale& c) {
     if (c.inv == 0.0f) return 0;        // zero or non-finite rows (uniform over the row)
-    const float t = __fmul_rn(fabsf(x), c.up);
-    float q = rintf(__fmul_rn(t, c.inv));
-    const float r2 = 2.0f * __fmaf_rn(-q, c.sm, t);
-    if (r2 >= c.sm) q += 1.0f;
-    else if (r2 < -c.sm) q -= 1.0f;
-    const int i = (int)fminf(q, 127.0f);
-    return x < 0.0f ? -i : i;
+    x = __fmul_rn(x, c.up);
+    return (int)fminf(fmaxf(code_settle(x, rintf(__fmul_rn(x, c.inv)), c), -127.0f), 127.0f);
 }
 
-// Reductions over the CTA, every thread getting the result, in a fixed order.
-// `red` holds two sets of 32 words used in turn, so that one barrier each is
-// enough.
+// Eight codes as two words.  Adding 1.5 * 2^23 rounds x * inv to a whole number
+// whose two's complement is the sum's low byte; the remainders' magnitudes are
+// compared with half a scale all eight at once, and only eight that have one at
+// or past it are settled one by one.  (bf16 rows have such border cases: half of
+// a row's largest value is 63.5 scales, and about one value in a thousand is it.)
+__device__ __forceinline__ uint2 codes8(const float (&v)[8], const CodeScale& c) {
+    if (c.inv == 0.0f) return make_uint2(0, 0);
+    uint32_t b[8];
+    if (c.up == 1.0f) {
+        float worst = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float t = __fmaf_rn(v[j], c.inv, 12582912.0f);
+            b[j] = __float_as_uint(t);
+            worst = fmaxf(worst, fabsf(__fmaf_rn(-__fsub_rn(t, 12582912.0f), c.sm, v[j])));
+        }
+        if (worst >= c.half) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float r = __fmaf_rn(-__fsub_rn(__uint_as_float(b[j]), 12582912.0f), c.sm, v[j]);
+                const float away = __uint_as_float(__float_as_uint(r) ^ (__float_as_uint(v[j]) & 0x80000000u));
+                const uint32_t one = v[j] < 0.0f ? ~0u : 1u;
+                if (away >= c.half) b[j] += one;
+                else if (away < -c.half) b[j] -= one;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) b[j] = (uint32_t)code_of(v[j], c);
+    }
+    return make_uint2(__byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410),
+                      __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410));
+}
+
+// Reductions over the threads of a row (blockDim.x, up to 16 warps; a CTA has
+// blockDim.y rows at a time), every thread getting the result, in a fixed order.
+// Two sets of 16 words are used in turn, so that one barrier a reduction is
+// enough; words of absent warps are zero.
+constexpr int kRowGroups = 8;           // most rows of a CTA at a time
+
 struct RowReduce {
-    uint32_t (*red)[32];
+    uint32_t (*red)[16];
     int turn;
+    __device__ __forceinline__ RowReduce(uint32_t (*r)[16]) : red(r + 2 * threadIdx.y), turn(0) {
+        if (threadIdx.x < 32) red[threadIdx.x >> 4][threadIdx.x & 15] = 0;
+        __syncthreads();
+    }
+    __device__ __forceinline__ const uint4* exchange(uint32_t v) {
+        uint32_t* r = red[turn];
+        turn ^= 1;
+        if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = v;
+        asm volatile("bar.sync %0, %1;" ::"r"(threadIdx.y + 1), "r"(blockDim.x) : "memory");
+        return reinterpret_cast<const uint4*>(r);
+    }
     __device__ __forceinline__ float sum(float v) {
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        const int nw = blockDim.x >> 5;
-        if (nw == 1) return v;
-        uint32_t* r = red[turn];
-        turn ^= 1;
-        if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = __float_as_uint(v);
-        __syncthreads();
+        if (blockDim.x == 32) return v;
+        const uint4* r = exchange(__float_as_uint(v));
         float s = 0.0f;
-        for (int i = 0; i < nw; ++i) s += __uint_as_float(r[i]);
+        for (int i = 0; i < (int)blockDim.x; i += 128) {
+            const uint4 w = r[i >> 7];
+            s += (__uint_as_float(w.x) + __uint_as_float(w.y)) + (__uint_as_float(w.z) + __uint_as_float(w.w));
+        }
         return s;
     }
     __device__ __forceinline__ uint32_t max(uint32_t v) {
         v = __reduce_max_sync(0xffffffffu, v);
-        const int nw = blockDim.x >> 5;
-        if (nw == 1) return v;
-        uint32_t* r = red[turn];
-        turn ^= 1;
-        if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = v;
-        __syncthreads();
+        if (blockDim.x == 32) return v;
+        const uint4* r = exchange(v);
         uint32_t m = 0;
-        for (int i = 0; i < nw; ++i) m = ::max(m, r[i]);
+        for (int i = 0; i < (int)blockDim.x; i += 128) {
+            const uint4 w = r[i >> 7];
+            m = ::max(m, ::max(::max(w.x, w.y), ::max(w.z, w.w)));
+        }
         return m;
     }
 };
 
-// Where a thread's values of a row lie.  VEC: chunk c of 8 consecutive values
-// from element 8 c; else value j of chunk c is element (8 (c / threads) + j) *
-// threads + c % threads, so that a warp's single-element accesses are
-// neighbours.  Past the row's end values count as 0 and nothing is written.
+// Where a thread's values of a row lie, chunk by chunk of eight.  VEC: its chunk
+// i is elements 8 c .. 8 c + 7 with c = i * threads + its number; else value j of
+// it is element (8 i + j) * threads + its number, so that a warp's single-element
+// accesses are neighbours.  Past the row's end values count as 0 and nothing is
+// written.
 template <bool VEC>
-__device__ __forceinline__ int elem(int c, int j) {
-    return VEC ? 8 * c + j : (int)(8 * (c / (int)blockDim.x) + j) * (int)blockDim.x + c % (int)blockDim.x;
+__device__ __forceinline__ int elem(int i, int j) {
+    return VEC ? 8 * (i * (int)blockDim.x + (int)threadIdx.x) + j : (8 * i + j) * (int)blockDim.x + (int)threadIdx.x;
 }
 
 template <bool VEC>
-__device__ __forceinline__ void get8(const void* p, int type, int64_t row0, int c, int cols, float (&v)[8]) {
-    if (VEC && 8 * c + 8 <= cols) {
-        load8(p, type, row0 + 8 * c, v);
+__device__ __forceinline__ void get8(const void* p, int type, int64_t row0, int i, int cols, float (&v)[8]) {
+    if (VEC && elem<VEC>(i, 0) + 8 <= cols) {
+        load8(p, type, row0 + elem<VEC>(i, 0), v);
+        return;
+    }
+    // all eight loads before any conversion, so that they are in flight together
+    if (type == ELQ_F32) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int e = elem<VEC>(i, j);
+            v[j] = e < cols ? reinterpret_cast<const float*>(p)[row0 + e] : 0.0f;
+        }
+        return;
+    }
+    uint32_t r[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int e = elem<VEC>(i, j);
+        r[j] = e < cols ? reinterpret_cast<const uint16_t*>(p)[row0 + e] : 0;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        v[j] = type == ELQ_BF16 ? bf16_lo(r[j]) : __half2float(__ushort_as_half((unsigned short)r[j]));
+}
+
+template <bool VEC>
+__device__ __forceinline__ void put8(void* p, int type, int64_t row0, int i, int cols, const float (&v)[8]) {
+    if (VEC && elem<VEC>(i, 0) + 8 <= cols) {
+        store8(p, type, row0 + elem<VEC>(i, 0), v);
+        return;
+    }
+    if (type == ELQ_F32) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (elem<VEC>(i, j) < cols) reinterpret_cast<float*>(p)[row0 + elem<VEC>(i, j)] = v[j];
         return;
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const int e = elem<VEC>(c, j);
-        v[j] = e < cols ? load1(p, type, row0 + e) : 0.0f;
+    for (int j = 0; j < 8; j += 2) {
+        const uint32_t w = type == ELQ_BF16 ? pack_bf16(v[j], v[j + 1]) : pack_f16(v[j], v[j + 1]);
+        uint16_t* d = reinterpret_cast<uint16_t*>(p) + row0;
+        if (elem<VEC>(i, j) < cols) d[elem<VEC>(i, j)] = (uint16_t)w;
+        if (elem<VEC>(i, j + 1) < cols) d[elem<VEC>(i, j + 1)] = (uint16_t)(w >> 16);
     }
 }
 
 template <bool VEC>
-__device__ __forceinline__ void put8(void* p, int type, int64_t row0, int c, int cols, const float (&v)[8]) {
-    if (VEC && 8 * c + 8 <= cols) {
-        store8(p, type, row0 + 8 * c, v);
-        return;
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const int e = elem<VEC>(c, j);
-        if (e < cols) store1(p, type, row0 + e, v[j]);
-    }
-}
-
-template <bool VEC>
-__device__ __forceinline__ void put_codes8(int8_t* q, int64_t row0, int c, int cols, const float (&v)[8],
+__device__ __forceinline__ void put_codes8(int8_t* q, int64_t row0, int i, int cols, const float (&v)[8],
                                            const CodeScale& cs) {
-    if (VEC && 8 * c + 8 <= cols) {
-        uint32_t w[2] = {0, 0};
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[j >> 2] |= (uint32_t)(code_of(v[j], cs) & 0xff) << (8 * (j & 3));
-        *reinterpret_cast<uint2*>(q + row0 + 8 * c) = make_uint2(w[0], w[1]);
+    if (VEC && elem<VEC>(i, 0) + 8 <= cols) {
+        *reinterpret_cast<uint2*>(q + row0 + elem<VEC>(i, 0)) = codes8(v, cs);
         return;
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const int e = elem<VEC>(c, j);
+        const int e = elem<VEC>(i, j);
         if (e < cols) q[row0 + e] = (int8_t)code_of(v[j], cs);
     }
 }
 
-__device__ __forceinline__ uint32_t amax8(uint32_t m, const float (&v)[8]) {
+// The larger of m and |v|, a NaN if either is one.
+__device__ __forceinline__ float amax8(float m, const float (&v)[8]) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
+    for (int j = 0; j < 8; ++j) asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(v[j])));
     return m;
 }
 
@@ -246,64 +330,94 @@ __device__ __forceinline__ float sumsq8(float s, const float (&v)[8]) {
     return s;
 }
 
-__device__ __forceinline__ float rstd_of(float ss, int cols, float eps) {
-    return __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(ss, (float)cols), eps)));
+// 1 / sqrt(mean + eps), by the reciprocal of the length and rsqrtf (2 ulp): the
+// row's factor within four roundings beside the sum's own.
+__device__ __forceinline__ float rstd_of(float ss, float inv_cols, float eps) {
+    return rsqrtf(__fmaf_rn(ss, inv_cols, eps));
 }
 
-// The eight source values of chunk c of output row `row` (the quantisers'
+// silu(g) * u to within 2^-21 of its value (or 2^-118 |u|, where g < -88).
+// exp(-g) = 2^n * 2^f with n whole and f reduced by a two-part log2(e); the
+// hardware's 2^f is good to 2^-22 and its reciprocal to 2^-23, both far below the
+// half step of the code that follows.
+__device__ __forceinline__ float swiglu1(float g, float u) {
+    const float z = fminf(fmaxf(-g, -87.0f), 88.0f);
+    const float n = rintf(__fmul_rn(z, 1.44269502f));
+    float f = __fmaf_rn(z, 1.44269502f, -n);
+    f = __fmaf_rn(z, 1.92596299e-8f, f);
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(f));
+    e = __fmul_rn(e, __int_as_float(((int)n + 127) << 23));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(__fadd_rn(1.0f, e)));
+    return __fmul_rn(__fmul_rn(g, r), u);
+}
+
+// The eight source values of chunk ci of output row `row` (the quantisers'
 // inputs before quantising, or the x of a norm).
 template <int OP, bool VEC>
-__device__ __forceinline__ void source8(const RowArgs& a, int64_t row, int64_t src, int c, float (&v)[8]) {
+__device__ __forceinline__ void source8(const RowArgs& a, int64_t row, int64_t src, int ci, float (&v)[8]) {
     if (OP == ROW_QUANT) {
         if (src < 0) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] = 0.0f;
         } else {
-            get8<VEC>(a.x, a.x_type, src * a.ldx, c, a.cols, v);
+            get8<VEC>(a.x, a.x_type, src * a.ldx, ci, a.cols, v);
         }
     } else if (OP == ROW_SWIGLU) {
         float u[8];
-        get8<VEC>(a.x, a.x_type, row * a.ldx, c, a.cols, v);
-        get8<VEC>(a.x, a.x_type, row * a.ldx + a.cols, c, a.cols, u);
+        get8<VEC>(a.x, a.x_type, row * a.ldx, ci, a.cols, v);
+        get8<VEC>(a.x, a.x_type, row * a.ldx + a.cols, ci, a.cols, u);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            // exp(-g) = inf gives g / inf = -0 for a very negative g
-            const float e = __expf(-v[j]);
-            v[j] = __fmul_rn(__fdiv_rn(v[j], __fadd_rn(1.0f, e)), u[j]);
+            v[j] = swiglu1(v[j], u[j]);
         }
     } else if (OP == ROW_COMBINE) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-        for (int i = 0; i < a.k; ++i) {
-            const int64_t p = a.index[row * a.k + i];
-            if (p < 0 || p >= a.x_rows) continue;
-            const float w = a.weights[row * a.k + i];
-            float o[8];
-            get8<VEC>(a.x, a.x_type, p * a.ldx, c, a.cols, o);
+        for (int i0 = 0; i0 < a.k; i0 += 4) {
+            float w[4], o[4][8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = __fmaf_rn(w, o[j], v[j]);
+            for (int i = 0; i < 4; ++i) {
+                const int64_t p = i0 + i < a.k ? a.index[row * a.k + i0 + i] : -1;
+                const bool on = p >= 0 && p < a.x_rows;
+                w[i] = on ? a.weights[row * a.k + i0 + i] : 0.0f;
+                if (on) {
+                    get8<VEC>(a.x, a.x_type, p * a.ldx, ci, a.cols, o[i]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) o[i][j] = 0.0f;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = __fmaf_rn(w[i], o[i][j], v[j]);
         }
     } else {
-        get8<VEC>(a.x, a.x_type, row * a.ldx, c, a.cols, v);
+        get8<VEC>(a.x, a.x_type, row * a.ldx, ci, a.cols, v);
     }
 }
 
 template <bool VEC>
-__device__ __forceinline__ void weight8(const float* w, int c, int cols, float (&v)[8]) {
+__device__ __forceinline__ void weight8(const float* w, int i, int cols, float (&v)[8]) {
     if (w) {
-        get8<VEC>(w, ELQ_F32, 0, c, cols, v);
+        get8<VEC>(w, ELQ_F32, 0, i, cols, v);
     } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = 1.0f;
     }
 }
 
+__device__ __forceinline__ float residual1(float y, float rstd, float w, float g, float res_scale, float h) {
+    return __fmaf_rn(g, __fmul_rn(__fmul_rn(y, rstd), w), __fmul_rn(res_scale, h));
+}
+
 // v (y's values) -> h' = res_scale * h + gate * (y * rstd * w); 0 past the end.
 template <bool VEC>
-__device__ __forceinline__ void residual8(const RowArgs& a, int64_t row, int c, float rstd, const float (&h)[8],
+__device__ __forceinline__ void residual8(const RowArgs& a, int64_t row, int i, float rstd, const float (&h)[8],
                                           float (&v)[8]) {
     float w[8], g[8];
-    weight8<VEC>(a.w, c, a.cols, w);
+    weight8<VEC>(a.w, i, a.cols, w);
     if (!a.gate) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) g[j] = 1.0f;
@@ -314,22 +428,21 @@ __device__ __forceinline__ void residual8(const RowArgs& a, int64_t row, int c, 
 #pragma unroll
             for (int j = 0; j < 8; ++j) g[j] = g0;
         } else {
-            get8<VEC>(gr, ELQ_F32, 0, c, a.cols, g);
+            get8<VEC>(gr, ELQ_F32, 0, i, a.cols, g);
         }
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const float n = __fmul_rn(__fmul_rn(v[j], rstd), w[j]);
-        const float r = __fmaf_rn(g[j], n, __fmul_rn(a.res_scale, h[j]));
-        v[j] = elem<VEC>(c, j) < a.cols ? r : 0.0f;
+        const float r = residual1(v[j], rstd, w[j], g[j], a.res_scale, h[j]);
+        v[j] = elem<VEC>(i, j) < a.cols ? r : 0.0f;
     }
 }
 
 // v -> v * rstd * w, the normalised row.
 template <bool VEC>
-__device__ __forceinline__ void norm8(const float* wt, int c, int cols, float rstd, float (&v)[8]) {
+__device__ __forceinline__ void norm8(const float* wt, int i, int cols, float rstd, float (&v)[8]) {
     float w[8];
-    weight8<VEC>(wt, c, cols, w);
+    weight8<VEC>(wt, i, cols, w);
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(__fmul_rn(v[j], rstd), w[j]);
 }
@@ -338,9 +451,9 @@ __device__ __forceinline__ void norm8(const float* wt, int c, int cols, float rs
 // or 0: none, every step reads its inputs again.
 template <int OP, int VPT, bool VEC>
 __global__ void __launch_bounds__(kRowThreads) k_rows(const __grid_constant__ RowArgs a) {
-    __shared__ uint32_t red[2][32];
-    RowReduce rr{red, 0};
-    const int nch = VEC ? (a.cols + 7) / 8 : (int)blockDim.x * (int)((a.cols + 8ll * blockDim.x - 1) / (8ll * blockDim.x));
+    __shared__ __align__(16) uint32_t red[2][16];
+    RowReduce rr(red);
+    const int nch = (int)((a.cols + 8ll * blockDim.x - 1) / (8ll * blockDim.x));      // chunks of a thread
     constexpr int NV = VPT > 0 ? VPT : 1;
     const bool codes = a.n_type == ELQ_I8;
     int8_t* q = reinterpret_cast<int8_t*>(a.n);
@@ -355,27 +468,25 @@ __global__ void __launch_bounds__(kRowThreads) k_rows(const __grid_constant__ Ro
             float h[OP == ROW_RESIDUAL ? NV : 1][8];
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int c = threadIdx.x + i * blockDim.x;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
-                if (c < nch) source8<OP, VEC>(a, row, src, c, v[i]);
+                if (i < nch) source8<OP, VEC>(a, row, src, i, v[i]);
                 if constexpr (OP == ROW_RESIDUAL) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) h[i][j] = 0.0f;
-                    if (c < nch) get8<VEC>(a.h, a.h_type, row * a.ldh, c, a.cols, h[i]);
+                    if (i < nch) get8<VEC>(a.h, a.h_type, row * a.ldh, i, a.cols, h[i]);
                 }
             }
             if constexpr (OP == ROW_RESIDUAL) {
                 float ss = 0.0f;
 #pragma unroll
                 for (int i = 0; i < NV; ++i) ss = sumsq8(ss, v[i]);
-                const float rstd = rstd_of(rr.sum(ss), a.cols, a.eps);
+                const float rstd = rstd_of(rr.sum(ss), a.inv_cols, a.eps);
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
-                    const int c = threadIdx.x + i * blockDim.x;
-                    if (c >= nch) continue;
-                    residual8<VEC>(a, row, c, rstd, h[i], v[i]);
-                    put8<VEC>(a.h_out, a.h_type, row * a.ld_out, c, a.cols, v[i]);
+                        if (i >= nch) continue;
+                    residual8<VEC>(a, row, i, rstd, h[i], v[i]);
+                    put8<VEC>(a.h_out, a.h_type, row * a.ld_out, i, a.cols, v[i]);
                 }
                 if (!a.n) continue;
             }
@@ -383,80 +494,320 @@ __global__ void __launch_bounds__(kRowThreads) k_rows(const __grid_constant__ Ro
                 float ss = 0.0f;
 #pragma unroll
                 for (int i = 0; i < NV; ++i) ss = sumsq8(ss, v[i]);
-                const float rstd = rstd_of(rr.sum(ss), a.cols, a.eps);
+                const float rstd = rstd_of(rr.sum(ss), a.inv_cols, a.eps);
                 const float* wt = OP == ROW_RMS ? a.w : a.w_next;
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
-                    const int c = threadIdx.x + i * blockDim.x;
-                    if (c >= nch) continue;
-                    norm8<VEC>(wt, c, a.cols, rstd, v[i]);
-                    if (!codes) put8<VEC>(a.n, a.n_type, row * a.ldn, c, a.cols, v[i]);
+                        if (i >= nch) continue;
+                    norm8<VEC>(wt, i, a.cols, rstd, v[i]);
+                    if (!codes) put8<VEC>(a.n, a.n_type, row * a.ldn, i, a.cols, v[i]);
                 }
                 if (!codes) continue;
             }
-            uint32_t m = 0;
+            float m = 0.0f;
 #pragma unroll
             for (int i = 0; i < NV; ++i) m = amax8(m, v[i]);
-            const CodeScale cs = code_scale(rr.max(m));
+            const CodeScale cs = code_scale(rr.max(__float_as_uint(m)));
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int c = threadIdx.x + i * blockDim.x;
-                if (c < nch) put_codes8<VEC>(q, row * a.ldn, c, a.cols, v[i], cs);
+                if (i < nch) put_codes8<VEC>(q, row * a.ldn, i, a.cols, v[i], cs);
             }
             if (threadIdx.x == 0) a.scale[row] = cs.s;
         } else {
             float(&t)[8] = v[0];
             float rstd = 0.0f, rstd2 = 0.0f;
-            // the row's values at chunk c: source, then the residual update,
+            // the row's values at chunk i: source, then the residual update,
             // as far as the statistics so far allow
-            auto value = [&](int c) {
-                source8<OP, VEC>(a, row, src, c, t);
+            auto value = [&](int i) {
+                source8<OP, VEC>(a, row, src, i, t);
                 if constexpr (OP == ROW_RESIDUAL) {
                     float h[8];
-                    get8<VEC>(a.h, a.h_type, row * a.ldh, c, a.cols, h);
-                    residual8<VEC>(a, row, c, rstd, h, t);
+                    get8<VEC>(a.h, a.h_type, row * a.ldh, i, a.cols, h);
+                    residual8<VEC>(a, row, i, rstd, h, t);
                 }
             };
             const float* wt = OP == ROW_RMS ? a.w : a.w_next;
             if constexpr (OP == ROW_RESIDUAL) {
                 float ss = 0.0f;
-                for (int c = threadIdx.x; c < nch; c += blockDim.x) {
-                    source8<OP, VEC>(a, row, src, c, t);
+                for (int i = 0; i < nch; ++i) {
+                    source8<OP, VEC>(a, row, src, i, t);
                     ss = sumsq8(ss, t);
                 }
-                rstd = rstd_of(rr.sum(ss), a.cols, a.eps);
+                rstd = rstd_of(rr.sum(ss), a.inv_cols, a.eps);
             }
             if (OP == ROW_RMS || (OP == ROW_RESIDUAL && a.n)) {
                 float ss = 0.0f;
-                for (int c = threadIdx.x; c < nch; c += blockDim.x) {
-                    value(c);
+                for (int i = 0; i < nch; ++i) {
+                    value(i);
                     ss = sumsq8(ss, t);
                 }
-                rstd2 = rstd_of(rr.sum(ss), a.cols, a.eps);
+                rstd2 = rstd_of(rr.sum(ss), a.inv_cols, a.eps);
             }
             CodeScale cs = code_scale(0);
             if (codes && a.n) {
-                uint32_t m = 0;
-                for (int c = threadIdx.x; c < nch; c += blockDim.x) {
-                    value(c);
-                    if (OP == ROW_RMS || OP == ROW_RESIDUAL) norm8<VEC>(wt, c, a.cols, rstd2, t);
+                float m = 0.0f;
+                for (int i = 0; i < nch; ++i) {
+                    value(i);
+                    if (OP == ROW_RMS || OP == ROW_RESIDUAL) norm8<VEC>(wt, i, a.cols, rstd2, t);
                     m = amax8(m, t);
                 }
-                cs = code_scale(rr.max(m));
+                cs = code_scale(rr.max(__float_as_uint(m)));
                 if (threadIdx.x == 0) a.scale[row] = cs.s;
             }
             // h_out may be h and n may be x: each element's inputs are read
             // here before its outputs are written, by the same thread
-            for (int c = threadIdx.x; c < nch; c += blockDim.x) {
-                value(c);
-                if (OP == ROW_RESIDUAL) put8<VEC>(a.h_out, a.h_type, row * a.ld_out, c, a.cols, t);
-                if (OP == ROW_RMS || (OP == ROW_RESIDUAL && a.n)) norm8<VEC>(wt, c, a.cols, rstd2, t);
+            for (int i = 0; i < nch; ++i) {
+                value(i);
+                if (OP == ROW_RESIDUAL) put8<VEC>(a.h_out, a.h_type, row * a.ld_out, i, a.cols, t);
+                if (OP == ROW_RMS || (OP == ROW_RESIDUAL && a.n)) norm8<VEC>(wt, i, a.cols, rstd2, t);
                 if (!a.n) continue;
-                if (codes) put_codes8<VEC>(q, row * a.ldn, c, a.cols, t, cs);
-                else put8<VEC>(a.n, a.n_type, row * a.ldn, c, a.cols, t);
+                if (codes) put_codes8<VEC>(q, row * a.ldn, i, a.cols, t, cs);
+                else put8<VEC>(a.n, a.n_type, row * a.ldn, i, a.cols, t);
             }
         }
     }
+}
+
+// ---- rows through shared memory ---------------------------------------------------
+//
+// What a row costs besides its values' arithmetic is kept small, since the codes'
+// rounding alone is some ten instructions a value and the SMs have about 30 to
+// give per value at HBM speed: a thread's pieces lie at fixed byte offsets (from
+// a row's start and in shared memory), their valid parts are worked out once, and
+// the copies' zero fill stands in for bounds checks when they are read back.
+
+// 16 bytes to shared memory, asynchronously; of the source only `bytes` are read
+// and the rest is zero.
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+    uint4 r;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a));
+    return r;
+}
+
+// The pieces of a row, in order: x's (SwiGLU: the gate's, then the up's), h's,
+// a gate that changes from row to row; and of the weights: the written norm's, and
+// the product of the post-norm's and a gate that all rows share.  Every fp32 chunk
+// of eight has two pieces, others one.
+inline __host__ __device__ constexpr int planes_of(int type) { return type == ELQ_F32 ? 2 : 1; }
+
+template <int VPT>
+struct Lane {
+    int nv[VPT];                // values of this thread's chunks
+    uint32_t first;             // shared-memory address of its first piece
+    int row_bytes16;            // bytes between its chunks at 16 bits a value: 16 * threads, also between pieces
+
+    // its chunks of a row at `src` into pieces from `at` on; `on` 0: zeros
+    __device__ __forceinline__ void fetch(uint32_t at, const uint8_t* src, int type, int on) const {
+        if (type == ELQ_F32) {
+            src += threadIdx.x * 32;
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                copy16(at + (2 * i) * row_bytes16, src + (int64_t)(2 * i) * row_bytes16, on * 4 * min(nv[i], 4));
+                copy16(at + (2 * i + 1) * row_bytes16, src + (int64_t)(2 * i) * row_bytes16 + 16,
+                       on * 4 * max(nv[i] - 4, 0));
+            }
+        } else {
+            src += threadIdx.x * 16;
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) copy16(at + i * row_bytes16, src + (int64_t)i * row_bytes16, on * 2 * nv[i]);
+        }
+    }
+    __device__ __forceinline__ void read(uint32_t at, int i, int type, float (&v)[8]) const {
+        if (type == ELQ_F32) {
+            const uint4 a = lds16(at + (2 * i) * row_bytes16), b = lds16(at + (2 * i + 1) * row_bytes16);
+            const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(w[j]);
+        } else {
+            widen8(lds16(at + i * row_bytes16), type, v);
+        }
+    }
+    // v to a row at dst (its first value), rounded to type
+    __device__ __forceinline__ void write(uint8_t* dst, int i, int type, const float (&v)[8]) const {
+        if (nv[i] == 8) {
+            if (type == ELQ_F32) store8(dst + threadIdx.x * 32 + (int64_t)(2 * i) * row_bytes16, type, 0, v);
+            else store8(dst + threadIdx.x * 16 + (int64_t)i * row_bytes16, type, 0, v);
+        } else {
+            const int e0 = 8 * threadIdx.x + i * (row_bytes16 >> 1);
+#pragma unroll
+            for (int j = 0; j < 7; ++j)
+                if (j < nv[i]) store1(dst, type, e0 + j, v[j]);
+        }
+    }
+    __device__ __forceinline__ void write_codes(int8_t* dst, int i, const float (&v)[8], const CodeScale& cs) const {
+        const int e0 = 8 * threadIdx.x + i * (row_bytes16 >> 1);
+        const uint2 w = codes8(v, cs);
+        if (nv[i] == 8) {
+            *reinterpret_cast<uint2*>(dst + e0) = w;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 7; ++j)
+                if (j < nv[i]) dst[e0 + j] = (int8_t)((j < 4 ? w.x : w.y) >> (8 * (j & 3)));
+        }
+    }
+};
+
+// A CTA works on blockDim.y rows at a time, blockDim.x threads each, which share
+// the weights in shared memory.  D stages: the rows in shared memory per row
+// worked on, D - 1 of them on their way.  XT: x's type, or 0xff: as x_type says.
+constexpr int kAnyType = 0xff;
+constexpr int kPipeThreads4 = 384;     // most threads with four chunks each
+
+template <int OP, int VPT, int D, int XT>
+__global__ void __launch_bounds__(VPT == 1 ? kRowThreads : kPipeThreads4, 2) k_pipe(const __grid_constant__ RowArgs a) {
+    extern __shared__ uint4 sm[];
+    __shared__ __align__(16) uint32_t red[2 * kRowGroups][16];
+    const int T = blockDim.x, xt = XT == kAnyType ? a.x_type : XT, ht = a.h_type;
+    Lane<VPT> ln;
+    ln.row_bytes16 = 16 * T;
+    ln.first = (uint32_t)__cvta_generic_to_shared(sm) + 16 * threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) ln.nv[i] = min(8, max(0, a.cols - 8 * ((int)threadIdx.x + i * T)));
+    const bool codes = a.n_type == ELQ_I8;
+    const bool gate_all = OP == ROW_RESIDUAL && a.gate && a.gate_cols > 1 && a.gate_rows >= a.rows;
+    const bool gate_row = OP == ROW_RESIDUAL && a.gate && a.gate_cols > 1 && a.gate_rows < a.rows;
+    const int plane = VPT * 16 * T;         // bytes of one piece of all the CTA's chunks
+    const int stage_bytes = a.row_planes * plane;
+    const uint32_t ring = ln.first + a.w_planes * plane + threadIdx.y * D * stage_bytes;
+    const int ox = planes_of(xt) * plane, oh = ox, og = ox + planes_of(ht) * plane;
+    const int64_t bx = a.ldx * (xt == ELQ_F32 ? 4 : 2), bh = a.ldh * (ht == ELQ_F32 ? 4 : 2);
+    const int64_t bo = a.ld_out * (ht == ELQ_F32 ? 4 : 2), bn = a.ldn * (codes ? 1 : a.n_type == ELQ_F32 ? 4 : 2);
+    const uint8_t* x = reinterpret_cast<const uint8_t*>(a.x);
+    const uint8_t* hp = reinterpret_cast<const uint8_t*>(a.h);
+    uint8_t* op = reinterpret_cast<uint8_t*>(a.h_out);
+    uint8_t* np = reinterpret_cast<uint8_t*>(a.n);
+
+    // the source row of an output row: -1 a gathered row that is not there, -2 past the end
+    auto source = [&](int64_t row) -> int64_t {
+        if (row >= a.rows) return -2;
+        if (OP != ROW_QUANT || !a.index) return row;
+        const int i = a.index[row];
+        return i < 0 || i / a.div >= a.x_rows ? -1 : i / a.div;
+    };
+    auto fetch = [&](uint32_t at, int64_t row, int64_t src) {
+        if (src != -2) {
+            const uint8_t* p = x + (src < 0 ? 0 : src) * bx;
+            ln.fetch(at, p, xt, OP != ROW_QUANT || src >= 0);
+            if (OP == ROW_SWIGLU) ln.fetch(at + ox, p + (int64_t)a.cols * (xt == ELQ_F32 ? 4 : 2), xt, 1);
+            if (OP == ROW_RESIDUAL) ln.fetch(at + oh, hp + src * bh, ht, 1);
+            if (gate_row)
+                ln.fetch(at + og, reinterpret_cast<const uint8_t*>(a.gate + (row / a.gate_rows) * a.gate_ld), ELQ_F32, 1);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+
+    int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    const int64_t step = (int64_t)gridDim.x * blockDim.y;
+    const float* w_last = OP == ROW_RMS ? a.w : a.n ? a.w_next : nullptr;     // of the norm that is written
+    const uint32_t w_first = ln.first + 2 * plane;                              // w * gate, where either is given
+    const bool wg = OP == ROW_RESIDUAL && (a.w || gate_all);
+    if (threadIdx.y == 0 && w_last)         // joins the first row's group
+        ln.fetch(ln.first, reinterpret_cast<const uint8_t*>(w_last), ELQ_F32, 1);
+#pragma unroll
+    for (int j = 0; j < D - 1; ++j) fetch(ring + j * stage_bytes, row + j * step, source(row + j * step));
+    int64_t ahead = source(row + (D - 1) * step);
+    if (wg && threadIdx.y == 0) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            float w[8], g[8];
+            weight8<true>(a.w, i, a.cols, w);
+            weight8<true>(gate_all ? a.gate : nullptr, i, a.cols, g);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = __fmul_rn(w[j], g[j]);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(w_first + (2 * i + j) * ln.row_bytes16),
+                             "f"(w[4 * j]), "f"(w[4 * j + 1]), "f"(w[4 * j + 2]), "f"(w[4 * j + 3])
+                             : "memory");
+        }
+    }
+    if ((OP == ROW_RMS || OP == ROW_RESIDUAL) && blockDim.y > 1)        // the other rows' threads read the weights too
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+    RowReduce rr(red);                                                  // a barrier of the CTA
+
+    for (int st = 0; row < a.rows; row += step, st = st + 1 == D ? 0 : st + 1) {
+        fetch(ring + (st == 0 ? D - 1 : st - 1) * stage_bytes, row + (D - 1) * step, ahead);
+        ahead = source(row + D * step);
+        asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
+        const uint32_t at = ring + st * stage_bytes;
+        float v[VPT][8];
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            ln.read(at, i, xt, v[i]);
+            if (OP == ROW_SWIGLU) {
+                float u[8];
+                ln.read(at + ox, i, xt, u);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[i][j] = swiglu1(v[i][j], u[j]);
+            }
+        }
+        if constexpr (OP == ROW_RESIDUAL) {
+            float ss = 0.0f;
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) ss = sumsq8(ss, v[i]);
+            const float rstd = rstd_of(rr.sum(ss), a.inv_cols, a.eps);
+            const float g0 = a.gate && a.gate_cols == 1 ? a.gate[(row / a.gate_rows) * a.gate_ld] : 1.0f;
+            uint8_t* o = op + row * bo;
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                float h[8], w[8];
+                // past the row's end y and h are 0, and so is h'
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[i][j] = __fmul_rn(v[i][j], rstd);
+                if (wg) {
+                    ln.read(w_first, i, ELQ_F32, w);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[i][j] = __fmul_rn(v[i][j], w[j]);
+                }
+                ln.read(at + oh, i, ht, h);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) h[j] = __fmul_rn(a.res_scale, h[j]);
+                if (gate_row) {
+                    ln.read(at + og, i, ELQ_F32, w);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[i][j] = __fmaf_rn(w[j], v[i][j], h[j]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[i][j] = __fmaf_rn(g0, v[i][j], h[j]);
+                }
+                ln.write(o, i, ht, v[i]);
+            }
+            if (!a.n) continue;
+        }
+        if constexpr (OP == ROW_RMS || OP == ROW_RESIDUAL) {
+            float ss = 0.0f;
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) ss = sumsq8(ss, v[i]);
+            const float rstd = rstd_of(rr.sum(ss), a.inv_cols, a.eps);
+            uint8_t* o = np + row * bn;
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[i][j] = __fmul_rn(v[i][j], rstd);
+                if (w_last) {
+                    float w[8];
+                    ln.read(ln.first, i, ELQ_F32, w);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[i][j] = __fmul_rn(v[i][j], w[j]);
+                }
+                if (!codes) ln.write(o, i, a.n_type, v[i]);
+            }
+            if (!codes) continue;
+        }
+        float m = 0.0f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) m = amax8(m, v[i]);
+        const CodeScale cs = code_scale(rr.max(__float_as_uint(m)));
+        int8_t* q = reinterpret_cast<int8_t*>(np) + row * bn;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) ln.write_codes(q, i, v[i], cs);
+        if (threadIdx.x == 0) a.scale[row] = cs.s;
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 }  // namespace elqops
