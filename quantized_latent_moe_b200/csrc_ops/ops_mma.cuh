@@ -183,6 +183,54 @@ __device__ __forceinline__ Unit unit_of(int u, const int* s_off, const int* s_ti
     return x;
 }
 
+// ---- epilogue ----------------------------------------------------------------------
+//
+// A lane has one channel and 32 rows.  Eight warps have the whole tile's outputs to
+// rescale and write while the next tile's MMAs run, so an output's share of
+// instructions decides whether they keep up: the output type is chosen once per 32,
+// the rows' scales come four at a time, and a row costs one pointer step.
+
+// The accumulators r of 32 rows as outputs: times the channel's and the rows'
+// scales (codes), plus the bias.
+template <int KIND>
+__device__ __forceinline__ void scale32(const uint32_t (&r)[32], const float* sx, float sw, float bias, bool add,
+                                        float (&v)[32]) {
+    if (KIND != KIND_I8) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+        const float4 s = *reinterpret_cast<const float4*>(sx + j);
+        v[j] = __fmul_rn(__fmul_rn((float)(int)r[j], sw), s.x);
+        v[j + 1] = __fmul_rn(__fmul_rn((float)(int)r[j + 1], sw), s.y);
+        v[j + 2] = __fmul_rn(__fmul_rn((float)(int)r[j + 2], sw), s.z);
+        v[j + 3] = __fmul_rn(__fmul_rn((float)(int)r[j + 3], sw), s.w);
+    }
+    if (add) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = __fadd_rn(v[j], bias);
+    }
+}
+
+__device__ __forceinline__ void put(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void put(__half* p, float v) { *p = __float2half_rn(v); }
+
+// v's first nr values to p, p + ld, ...
+template <typename T>
+__device__ __forceinline__ void write32(T* p, int64_t ld, int nr, const float (&v)[32]) {
+    if (nr == 32) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j, p += ld) put(p, v[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 31; ++j, p += ld)
+            if (j < nr) put(p, v[j]);
+    }
+}
+
 template <int KIND>
 __global__ void __launch_bounds__(kMmaThreads, 1) k_mma(const __grid_constant__ MmaArgs a) {
     extern __shared__ uint8_t smem[];
@@ -330,24 +378,16 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_mma(const __grid_constant__ 
                 const int nr = min(32, x.rows - c);
                 if (KIND == KIND_I8) {
                     __syncwarp();
-                    if (lane < nr) sx[lane] = __ldg(a.sx + x.row0 + c + lane);
+                    sx[lane] = lane < nr ? __ldg(a.sx + x.row0 + c + lane) : 0.0f;
                     __syncwarp();
                 }
+                float v[32];
+                scale32<KIND>(r, sx, sw, bias, a.bias != nullptr, v);
                 if (n < a.N) {
                     const int64_t at = (int64_t)(x.row0 + c) * a.ldy + n;
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        if (j < nr) {
-                            float v;
-                            if (KIND == KIND_I8) {
-                                v = __fmul_rn(__fmul_rn((float)(int)r[j], sw), sx[j]);
-                                if (a.bias) v = __fadd_rn(v, bias);
-                            } else {
-                                v = __uint_as_float(r[j]);
-                            }
-                            store1(a.y, a.y_type, at + j * a.ldy, v);
-                        }
-                    }
+                    if (a.y_type == ELQ_F32) write32(reinterpret_cast<float*>(a.y) + at, a.ldy, nr, v);
+                    else if (a.y_type == ELQ_BF16) write32(reinterpret_cast<__nv_bfloat16*>(a.y) + at, a.ldy, nr, v);
+                    else write32(reinterpret_cast<__half*>(a.y) + at, a.ldy, nr, v);
                 }
                 __syncwarp();
             }
