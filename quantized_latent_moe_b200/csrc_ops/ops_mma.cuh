@@ -37,6 +37,7 @@ using elq::smem_addr;
 __device__ int g_ops_err;
 
 constexpr uint64_t kOpsWaitNs = 2000000000ull;     // 2 s per bounded device wait
+constexpr uint64_t kOpsDrainNs = 100000000ull;     // 0.1 s for what is in flight after one ran out
 constexpr int kMmaThreads = 384;
 constexpr int kMmaEpiWarps = 8;
 constexpr int kMmaStagesMax = 16;
@@ -53,7 +54,7 @@ struct alignas(64) MmaArgs {
     CUtensorMap tx;             // activations [M][K], box 128 bytes x 32 rows
     const int32_t* offsets;     // NULL: one group of all M rows
     int M, E, N, Kb;
-    int bn;                     // most rows of a tile: a multiple of 32, <= 256
+    int bn;                     // most rows of a tile: a multiple of 32 a CTA, <= 256
     int stages;
     uint32_t idesc;             // instruction descriptor without its N field
     const float* sx;
@@ -66,53 +67,131 @@ struct alignas(64) MmaArgs {
 
 // ---- tcgen05 primitives --------------------------------------------------------
 
+template <int CG>
 __device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t cols) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(dst)), "r"(cols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    if constexpr (CG == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(dst)), "r"(cols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(dst)), "r"(cols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
 }
+template <int CG>
 __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+    if constexpr (CG == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+    else
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
 }
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-template <int KIND>
+template <int KIND, int CG>
 __device__ __forceinline__ void umma(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t acc) {
-    if constexpr (KIND == KIND_I8)
+    if constexpr (KIND == KIND_I8 && CG == 1)
         asm volatile(
             "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
             "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
             "l"(ad), "l"(bd), "r"(idesc), "r"(acc)
             : "memory");
-    else
+    else if constexpr (KIND == KIND_I8)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(ad), "l"(bd), "r"(idesc), "r"(acc)
+            : "memory");
+    else if constexpr (CG == 1)
         asm volatile(
             "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
             "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
             "l"(ad), "l"(bd), "r"(idesc), "r"(acc)
             : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(ad), "l"(bd), "r"(idesc), "r"(acc)
+            : "memory");
 }
+// An arrival on the barrier (in a pair: on both CTAs' barriers at this offset)
+// when all MMAs issued so far are done.
+template <int CG>
 __device__ __forceinline__ void umma_commit(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
-                 : "memory");
+    if constexpr (CG == 1)
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+                     : "memory");
+    else
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                smem_addr(bar)),
+            "h"((uint16_t)3)
+            : "memory");
+}
+// One lane of the warp.  Chosen by elect.sync, not by its number: the compiler then
+// knows that a single thread issues what follows, and keeps the MMAs' operands in
+// uniform registers (an MMA of 32 rows is issued every 21 ns; behind `lane == 0`
+// every 80 to 100, which bounded whole products).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The cluster address of the pair's first CTA's copy of a shared-memory object.
+__device__ __forceinline__ uint32_t first_cta(const void* p) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_addr(p)));
+    return r;
+}
+__device__ __forceinline__ void bar_arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void bar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
-__device__ __forceinline__ void copy_2d(void* dst, const CUtensorMap* m, int c0, int c1, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
-        "[%4];" ::"r"(smem_addr(dst)),
-        "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(smem_addr(bar))
-        : "memory");
+// Tensor-map copies into this CTA's shared memory; `bar` is a cluster address, in
+// a pair of the first CTA's barrier.  No multicast.
+template <int CG>
+__device__ __forceinline__ void copy_2d(uint32_t dst, const CUtensorMap* m, int c0, int c1, uint32_t bar) {
+    if constexpr (CG == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+            "[%4];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, "
+            "{%2, %3}], [%4];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(bar)
+            : "memory");
 }
-__device__ __forceinline__ void copy_3d(void* dst, const CUtensorMap* m, int c0, int c1, int c2, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
-        "[%5];" ::"r"(smem_addr(dst)),
-        "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_addr(bar))
-        : "memory");
+template <int CG>
+__device__ __forceinline__ void copy_3d(uint32_t dst, const CUtensorMap* m, int c0, int c1, int c2, uint32_t bar) {
+    if constexpr (CG == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+            "[%5];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, "
+            "{%2, %3, %4}], [%5];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+            : "memory");
 }
 
 // 32 consecutive 32-bit TMEM columns of this thread's lane.
@@ -135,16 +214,19 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t addr) {
     return (uint64_t)((addr >> 4) & 0x3fff) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
 }
 
-// Instruction descriptor without N: M = 128, both operands K-major.
-__host__ __device__ constexpr uint32_t mma_idesc(int kind) {
-    return ((uint32_t)(kTileCh >> 4) << 24) |
+// Instruction descriptor without N: M = 128 channels a CTA, both operands K-major.
+__host__ __device__ constexpr uint32_t mma_idesc(int kind, int cg) {
+    return ((uint32_t)(cg * kTileCh >> 4) << 24) |
            (kind == KIND_I8 ? (2u << 4) | (1u << 7) | (1u << 10)
                             : (1u << 4) | (kind == KIND_BF16 ? (1u << 7) | (1u << 10) : 0u));
 }
 
-// Bounded wait for an mbarrier phase; gives up at once when another role has.
+// Bounded wait for an mbarrier phase; gives up at once when another role has.  The
+// clock is read only once a wait is long: reading it costs as much as a whole
+// step of the pipeline.
 __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatile int* abort_v) {
-    if (mbar_try_wait(bar, parity)) return true;
+    for (int i = 0; i < 32; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = global_timer_ns();
     for (uint32_t i = 0; i < (1u << 26); ++i) {
         if (mbar_try_wait_hint(bar, parity, 20000u)) return true;
@@ -162,8 +244,11 @@ struct Unit {
     int e, ch0, row0, rows, n;      // expert, first channel, first row, rows, the MMA's N
 };
 
-// s_off: the clamped offsets; s_tile[e]: row tiles of the experts before e.
+// s_off: the clamped offsets; s_tile[e]: row tiles of the experts before e; tiles
+// have rows in steps of 16 (32 in a pair, where each CTA brings half of them).
+template <int CG>
 __device__ __forceinline__ Unit unit_of(int u, const int* s_off, const int* s_tile, int E, int ch_tiles) {
+    constexpr int step = 16 * CG;
     const int b = u / ch_tiles;
     int lo = 0, hi = E;             // the last e with s_tile[e] <= b
     while (hi - lo > 1) {
@@ -173,13 +258,13 @@ __device__ __forceinline__ Unit unit_of(int u, const int* s_off, const int* s_ti
     }
     const int nt = s_tile[lo + 1] - s_tile[lo], r = u - s_tile[lo] * ch_tiles;
     const int ct = r / nt, t = r - ct * nt, cnt = s_off[lo + 1] - s_off[lo];
-    const int bn = ((cnt + nt - 1) / nt + 15) & ~15;        // the group's rows in nt even tiles
+    const int bn = ((cnt + nt - 1) / nt + step - 1) & ~(step - 1);     // the group's rows in nt even tiles
     Unit x;
     x.e = lo;
-    x.ch0 = ct * kTileCh;
+    x.ch0 = ct * kTileCh * CG;
     x.row0 = s_off[lo] + t * bn;
     x.rows = min(bn, cnt - t * bn);
-    x.n = (x.rows + 15) & ~15;
+    x.n = (x.rows + step - 1) & ~(step - 1);
     return x;
 }
 
@@ -231,7 +316,12 @@ __device__ __forceinline__ void write32(T* p, int64_t ld, int nr, const float (&
     }
 }
 
-template <int KIND>
+// CG = 2: a pair of CTAs (a cluster, on the two SMs that share a tensor-core pair)
+// works on 256 channels by up to 256 rows as one MMA: each CTA brings its own 128
+// channels and half of the rows, so that a row travels from L2 to shared memory
+// half as often.  The first CTA issues the MMAs; its barriers count both CTAs'
+// copies and both epilogues.
+template <int KIND, int CG>
 __global__ void __launch_bounds__(kMmaThreads, 1) k_mma(const __grid_constant__ MmaArgs a) {
     extern __shared__ uint8_t smem[];
     uint64_t* full = reinterpret_cast<uint64_t*>(smem);
@@ -245,8 +335,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_mma(const __grid_constant__ 
     int* s_off = reinterpret_cast<int*>(smem + kMmaHdr);
     int* s_tile = s_off + a.E + 1;
     const uint32_t tiles0 = (smem_addr(s_tile + a.E + 1) + 1023u) & ~1023u;
-    uint8_t* ring = smem + (tiles0 - smem_addr(smem));
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kMmaStagesMax; ++i) {
@@ -255,13 +344,13 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_mma(const __grid_constant__ 
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(tfull + i, 1);
-            mbar_init(tempty + i, kMmaEpiWarps);
+            mbar_init(tempty + i, kMmaEpiWarps * CG);
         }
         mbar_init(drain, 1);
         *abort_v = 0;
         fence_barrier_init();
     }
-    if (warp == 2) tmem_alloc(s_tmem, 512);
+    if (warp == 2) tmem_alloc<CG>(s_tmem, 512);
     for (int i = threadIdx.x; i <= a.E; i += kMmaThreads)
         s_off[i] = a.offsets ? clamp_offset(__ldg(a.offsets + i), a.M) : (i ? a.M : 0);
     __syncthreads();
@@ -281,32 +370,35 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_mma(const __grid_constant__ 
         }
         if (lane == 0) s_tile[a.E] = before;
     }
+    __syncwarp();
     tc_before();
-    __syncthreads();
+    if (CG == 1) __syncthreads();
+    else cluster_sync();
     tc_after();
     const uint32_t tmem = *s_tmem;
-    const int ch_tiles = (a.N + kTileCh - 1) / kTileCh;
+    const int ch_tiles = (a.N + CG * kTileCh - 1) / (CG * kTileCh);
     const int units = s_tile[a.E] * ch_tiles;
     const int steps = (a.Kb + kStepBytes - 1) / kStepBytes;
-    const int stage_bytes = kABytes + a.bn * kStepBytes;
+    const int stage_bytes = kABytes + a.bn / CG * kStepBytes;
+    const int rank = CG == 1 ? 0 : (int)cluster_rank(), u0 = blockIdx.x / CG, du = gridDim.x / CG;
 
     if (warp == 0) {
-        if (lane == 0) {
+        if (elect_one()) {
             int st = 0;
             uint32_t ph = 0;
             long long issued = 0;
             bool ok = true;
-            for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
-                const Unit x = unit_of(u, s_off, s_tile, a.E, ch_tiles);
-                const int boxes = (x.n + kBoxRows - 1) / kBoxRows;
+            for (int u = u0; ok && u < units; u += du) {
+                const Unit x = unit_of<CG>(u, s_off, s_tile, a.E, ch_tiles);
+                const int boxes = (x.n / CG + kBoxRows - 1) / kBoxRows, row0 = x.row0 + rank * (x.n / CG);
                 for (int k = 0; k < steps; ++k) {
                     if (!(ok = bar_wait(empty + st, ph ^ 1, abort_v))) break;
-                    uint8_t* p = ring + st * stage_bytes;
+                    const uint32_t p = tiles0 + st * stage_bytes, fb = CG == 1 ? smem_addr(full + st) : first_cta(full + st);
                     const int c = k * (KIND == KIND_I8 ? kStepBytes : kStepBytes / 2);
-                    mbar_arrive_expect_tx(full + st, kABytes + boxes * kBoxBytes);
-                    copy_3d(p, &a.tw, c, x.ch0, x.e, full + st);
+                    if (rank == 0) mbar_arrive_expect_tx(full + st, CG * (kABytes + boxes * kBoxBytes));
+                    copy_3d<CG>(p, &a.tw, c, x.ch0 + rank * kTileCh, x.e, fb);
                     for (int b = 0; b < boxes; ++b)
-                        copy_2d(p + kABytes + b * kBoxBytes, &a.tx, c, x.row0 + b * kBoxRows, full + st);
+                        copy_2d<CG>(p + kABytes + b * kBoxBytes, &a.tx, c, row0 + b * kBoxRows, fb);
                     ++issued;
                     if (++st == a.stages) {
                         st = 0;
@@ -315,23 +407,24 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_mma(const __grid_constant__ 
                 }
             }
             if (!ok) {
-                // let the copies in flight land before the CTA gives up its memory
+                // let the copies in flight land before the CTA gives up its memory (a pair's second CTA cannot
+                // see them land: it gives them the whole time)
                 for (int i = 0; i < a.stages && i < issued; ++i) {
                     const long long n = issued - 1 - i;
                     const uint64_t t0 = global_timer_ns();
-                    while (!mbar_try_wait_hint(full + n % a.stages, (uint32_t)(n / a.stages) & 1, 20000u) &&
-                           global_timer_ns() - t0 < kOpsWaitNs) {
+                    while (!(rank == 0 && mbar_try_wait_hint(full + n % a.stages, (uint32_t)(n / a.stages) & 1, 20000u)) &&
+                           global_timer_ns() - t0 < kOpsDrainNs) {
                     }
                 }
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (rank == 0 && elect_one()) {
             int st = 0, it = 0;
             uint32_t ph = 0;
             bool ok = true;
-            for (int u = blockIdx.x; ok && u < units; u += gridDim.x, ++it) {
-                const Unit x = unit_of(u, s_off, s_tile, a.E, ch_tiles);
+            for (int u = u0; ok && u < units; u += du, ++it) {
+                const Unit x = unit_of<CG>(u, s_off, s_tile, a.E, ch_tiles);
                 const int acc = it & 1;
                 if (!(ok = bar_wait(tempty + acc, ((it >> 1) & 1) ^ 1, abort_v))) break;
                 tc_after();
@@ -342,19 +435,24 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_mma(const __grid_constant__ 
                     const uint32_t p = tiles0 + st * stage_bytes;
                     const uint64_t ad = sw128_desc(p), bd = sw128_desc(p + kABytes);
                     const int parts = min(4, (a.Kb - k * kStepBytes + 31) / 32);
-                    for (int i = 0; i < parts; ++i) umma<KIND>(d, ad + 2 * i, bd + 2 * i, idesc, k > 0 || i > 0);
-                    umma_commit(empty + st);
+                    if (parts == 4) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) umma<KIND, CG>(d, ad + 2 * i, bd + 2 * i, idesc, k > 0 || i > 0);
+                    } else {
+                        for (int i = 0; i < parts; ++i) umma<KIND, CG>(d, ad + 2 * i, bd + 2 * i, idesc, k > 0 || i > 0);
+                    }
+                    umma_commit<CG>(empty + st);
                     if (++st == a.stages) {
                         st = 0;
                         ph ^= 1;
                     }
                 }
-                if (ok) umma_commit(tfull + acc);
+                if (ok) umma_commit<CG>(tfull + acc);
             }
             if (!ok) {
-                umma_commit(drain);
+                umma_commit<CG>(drain);
                 const uint64_t t0 = global_timer_ns();
-                while (!mbar_try_wait_hint(drain, 0, 20000u) && global_timer_ns() - t0 < kOpsWaitNs) {
+                while (!mbar_try_wait_hint(drain, 0, 20000u) && global_timer_ns() - t0 < kOpsDrainNs) {
                 }
             }
         }
@@ -362,9 +460,9 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_mma(const __grid_constant__ 
         const int q = warp & 3, half = (warp - 4) >> 2;
         float* sx = s_sx + (warp - 4) * 32;
         int it = 0;
-        for (int u = blockIdx.x; u < units; u += gridDim.x, ++it) {
-            const Unit x = unit_of(u, s_off, s_tile, a.E, ch_tiles);
-            const int acc = it & 1, n = x.ch0 + q * 32 + lane;
+        for (int u = u0; u < units; u += du, ++it) {
+            const Unit x = unit_of<CG>(u, s_off, s_tile, a.E, ch_tiles);
+            const int acc = it & 1, n = x.ch0 + rank * kTileCh + q * 32 + lane;
             float sw = 1.0f, bias = 0.0f;
             if (KIND == KIND_I8 && n < a.N) {
                 sw = __ldg(a.sw + (int64_t)x.e * a.N + n);
@@ -393,14 +491,18 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_mma(const __grid_constant__ 
             }
             tc_before();
             __syncwarp();
-            if (lane == 0) bar_arrive(tempty + acc);
+            if (lane == 0) {
+                if (CG == 1) bar_arrive(tempty + acc);
+                else bar_arrive_cluster(first_cta(tempty + acc));
+            }
         }
     }
     __syncwarp();
     tc_before();
-    __syncthreads();
+    if (CG == 1) __syncthreads();
+    else cluster_sync();        // neither CTA leaves while the other may still reach its memory
     tc_after();
-    if (warp == 2) tmem_free(tmem, 512);
+    if (warp == 2) tmem_free<CG>(tmem, 512);
 }
 
 }  // namespace elqops
