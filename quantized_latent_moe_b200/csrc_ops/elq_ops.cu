@@ -265,46 +265,98 @@ int row_tile(const Product& p, int sms, int cg) {
     return bn;
 }
 
-template <int KIND, int CG>
-elq_status launch_mma(const Product& p, cudaStream_t s) {
+// The arguments that the tensor-core kernels share, but for the tile and ring.
+template <int KIND>
+bool mma_args(const Product& p, int cg, MmaArgs& a) {
     const int es = KIND == KIND_I8 ? 1 : 2;
-    const int sms = device_sms() / CG * CG;
-    const int64_t ch_tiles = ((int64_t)p.N + CG * kTileCh - 1) / (CG * kTileCh);
-    MmaArgs a;
     const cuuint64_t dw[3] = {(cuuint64_t)p.K, (cuuint64_t)p.N, (cuuint64_t)p.E};
     const cuuint64_t sw[2] = {(cuuint64_t)(p.ldw * es), (cuuint64_t)((p.E > 1 ? p.w_stride : p.ldw * p.N) * es)};
     const cuuint32_t bw[3] = {(cuuint32_t)(kStepBytes / es), kTileCh, 1};
     const cuuint64_t dx[2] = {(cuuint64_t)p.K, (cuuint64_t)p.M};
     const cuuint64_t sx[1] = {(cuuint64_t)(p.ldx * es)};
     const cuuint32_t bx[2] = {(cuuint32_t)(kStepBytes / es), kBoxRows};
-    if (!encode(&a.tw, es, 3, p.w, dw, sw, bw) || !encode(&a.tx, es, 2, p.x, dx, sx, bx)) return ELQ_ERR_CUDA;
     a.offsets = p.offsets;
     a.M = p.M;
     a.E = p.E;
     a.N = p.N;
     a.Kb = p.K * es;
-    a.bn = row_tile(p, sms, CG);
-    const int64_t units = ((int64_t)p.M / a.bn + p.E + 1) * ch_tiles;
-    if (units > INT32_MAX) return ELQ_ERR_UNSUPPORTED;
-    const int hdr = kMmaHdr + 2 * (p.E + 1) * 4 + 1024, stage = kABytes + a.bn / CG * kStepBytes;
-    a.stages = std::min(kMmaStagesMax, (kMmaSmemMax - hdr) / stage);
-    a.idesc = mma_idesc(KIND, CG);
+    a.split = 1;
+    a.idesc = mma_idesc(KIND, cg);
     a.sx = p.sx;
     a.sw = p.sw;
     a.bias = p.bias;
     a.y = p.y;
     a.y_type = p.y_type;
     a.ldy = p.ldy;
-    static bool optin[kMaxDevices];
+    return encode(&a.tw, es, 3, p.w, dw, sw, bw) && encode(&a.tx, es, 2, p.x, dx, sx, bx);
+}
+
+// Large shared memory for a kernel, once per device.
+template <typename K>
+bool mma_optin(K kern, bool* done) {
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return ELQ_ERR_CUDA;
-    if (dev < 0 || dev >= kMaxDevices || !optin[dev]) {
-        if (cudaFuncSetAttribute(k_mma<KIND, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMmaSmemMax) != cudaSuccess)
-            return ELQ_ERR_CUDA;
-        if (dev >= 0 && dev < kMaxDevices) optin[dev] = true;
-    }
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    if (dev >= 0 && dev < kMaxDevices && done[dev]) return true;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMmaSmemMax) != cudaSuccess) return false;
+    if (dev >= 0 && dev < kMaxDevices) done[dev] = true;
+    return true;
+}
+
+template <int KIND, int CG>
+elq_status launch_mma(const Product& p, cudaStream_t s) {
+    static bool optin[kMaxDevices];
+    const int sms = device_sms() / CG * CG;
+    const int64_t ch_tiles = ((int64_t)p.N + CG * kTileCh - 1) / (CG * kTileCh);
+    MmaArgs a;
+    if (!mma_args<KIND>(p, CG, a) || !mma_optin(k_mma<KIND, CG>, optin)) return ELQ_ERR_CUDA;
+    a.bn = row_tile(p, sms, CG);
+    const int64_t units = ((int64_t)p.M / a.bn + p.E + 1) * ch_tiles;
+    if (units > INT32_MAX) return ELQ_ERR_UNSUPPORTED;
+    const int hdr = kMmaHdr + 2 * (p.E + 1) * 4 + 1024, stage = kABytes + a.bn / CG * kStepBytes;
+    a.stages = std::min(kMmaStagesMax, (kMmaSmemMax - hdr) / stage);
     const dim3 grid((unsigned)std::min<int64_t>(sms, units * CG));
     return status_of(launch(k_mma<KIND, CG>, grid, kMmaThreads, (size_t)(hdr + a.stages * stage), s, a, CG));
+}
+
+// CTAs per tile and rows of a tile for a dense product split over K; 1 where no
+// split is quicker.  In nanoseconds, as measured: a K step of a lone tile of bn
+// rows takes 150 + 0.4 bn, the exchange 400 + 17 a row.  (4096 -> 1792: 16 rows
+// 6.6 us against 10.4 unsplit, 256 rows 9.0 against 12.5; from about 1000 rows on
+// the tiles fill the SMs.)
+int split_plan(const Product& p, int es, int* bn) {
+    const int sms = device_sms(), steps = (int)(((int64_t)p.K * es + kStepBytes - 1) / kStepBytes);
+    const int64_t ch_tiles = ((int64_t)p.N + kTileCh - 1) / kTileCh;
+    const int bn1 = row_tile(p, sms, 1);
+    if ((p.M + bn1 - 1) / bn1 * ch_tiles > sms) return 1;
+    int best = 1;
+    int64_t cost = (int64_t)steps * (150 + bn1 * 2 / 5);
+    for (int t = 32; t <= 256 && t < p.M + 32; t += 32) {
+        const int64_t tiles = (p.M + t - 1) / t * ch_tiles;
+        for (int split = 2; split <= 8 && split <= steps && tiles * split <= sms; split *= 2) {
+            const int64_t c = (int64_t)((steps + split - 1) / split) * (150 + t * 2 / 5) + 400 + 17 * std::min(t, p.M);
+            if (c < cost) {
+                cost = c;
+                best = split;
+                *bn = t;
+            }
+        }
+    }
+    return best;
+}
+
+template <int KIND>
+elq_status launch_split(const Product& p, int split, int bn, cudaStream_t s) {
+    static bool optin[kMaxDevices];
+    MmaArgs a;
+    if (!mma_args<KIND>(p, 1, a) || !mma_optin(k_split<KIND>, optin)) return ELQ_ERR_CUDA;
+    const int stage = kABytes + bn * kStepBytes, hdr = 512 + 1024;
+    const int steps = (int)((a.Kb + kStepBytes - 1) / kStepBytes), share = (steps + split - 1) / split;
+    a.bn = bn;
+    a.split = split;
+    a.stages = std::min({kMmaStagesMax, (kMmaSmemMax - hdr) / stage, share});
+    const int smem = hdr + std::max(a.stages * stage, bn * kTileCh * 4);
+    const int64_t tiles = (p.M + bn - 1) / bn * (((int64_t)p.N + kTileCh - 1) / kTileCh);
+    return status_of(launch(k_split<KIND>, dim3((unsigned)(tiles * split)), kMmaThreads, smem, s, a, split));
 }
 
 // Pairs of CTAs where their tiles (an expert with rows has one at least) fill the
@@ -314,6 +366,11 @@ elq_status launch_mma(const Product& p, cudaStream_t s) {
 // 1792 x 4096: 16.7 against 18.2).
 template <int KIND>
 elq_status launch_mma(const Product& p, cudaStream_t s) {
+    if (!p.offsets) {
+        int bn = 0;
+        const int split = split_plan(p, KIND == KIND_I8 ? 1 : 2, &bn);
+        if (split > 1) return launch_split<KIND>(p, split, bn, s);
+    }
     const int64_t pairs = ((int64_t)p.N + 2 * kTileCh - 1) / (2 * kTileCh);
     const int64_t row_tiles = std::max<int64_t>(std::min(p.E, p.M), (p.M + 255) / 256);
     return pairs * row_tiles > device_sms() / 2 ? launch_mma<KIND, 2>(p, s) : launch_mma<KIND, 1>(p, s);

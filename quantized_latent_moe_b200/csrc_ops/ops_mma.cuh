@@ -56,6 +56,7 @@ struct alignas(64) MmaArgs {
     int M, E, N, Kb;
     int bn;                     // most rows of a tile: a multiple of 32 a CTA, <= 256
     int stages;
+    int split;                  // k_split: CTAs of a tile
     uint32_t idesc;             // instruction descriptor without its N field
     const float* sx;
     const float* sw;
@@ -503,6 +504,198 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_mma(const __grid_constant__ 
     else cluster_sync();        // neither CTA leaves while the other may still reach its memory
     tc_after();
     if (warp == 2) tmem_free<CG>(tmem, 512);
+}
+
+// ---- split over K ------------------------------------------------------------------
+//
+// A dense product with few tiles would leave most SMs idle and run each tile's K
+// steps one after another.  Here a cluster of up to eight CTAs works on one tile,
+// each on its share of the K steps; the partial accumulators go to shared memory
+// and every CTA adds up and writes its share of the rows, reading the others'
+// partials through distributed shared memory in rank order (so the result does
+// not depend on timing).  Bound by latency: launch, one memory round trip, the
+// steps of a share, one exchange.
+template <int KIND>
+__global__ void __launch_bounds__(kMmaThreads, 1) k_split(const __grid_constant__ MmaArgs a) {
+    extern __shared__ uint8_t smem[];
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem);
+    uint64_t* empty = full + kMmaStagesMax;
+    uint64_t* tfull = empty + kMmaStagesMax;
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(tfull + 1);
+    volatile int* abort_v = reinterpret_cast<volatile int*>(s_tmem + 1);
+    const uint32_t tiles0 = (smem_addr(smem) + 512 + 1023u) & ~1023u;
+    const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+    const int S = a.split, rank = (int)cluster_rank(), tile = blockIdx.x / S;
+    const int ch_tiles = (a.N + kTileCh - 1) / kTileCh;
+    const int ch0 = tile % ch_tiles * kTileCh, row0 = tile / ch_tiles * a.bn, rows = min(a.bn, a.M - row0);
+    const int n = (rows + 15) & ~15, boxes = (n + kBoxRows - 1) / kBoxRows;
+    const int steps = (a.Kb + kStepBytes - 1) / kStepBytes;
+    const int k0 = (int)((int64_t)steps * rank / S), k1 = (int)((int64_t)steps * (rank + 1) / S);
+    const int stage_bytes = kABytes + a.bn * kStepBytes;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < a.stages; ++i) {
+            mbar_init(full + i, 1);
+            mbar_init(empty + i, 1);
+        }
+        mbar_init(tfull, 1);
+        *abort_v = 0;
+        fence_barrier_init();
+    }
+    if (warp == 2) tmem_alloc<1>(s_tmem, 256);
+    __syncwarp();
+    tc_before();
+    __syncthreads();
+    tc_after();
+    const uint32_t tmem = *s_tmem;
+
+    if (warp == 0) {
+        if (elect_one()) {
+            int st = 0, issued = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            for (int k = k0; k < k1; ++k) {
+                if (!(ok = bar_wait(empty + st, ph ^ 1, abort_v))) break;
+                const uint32_t p = tiles0 + st * stage_bytes, fb = smem_addr(full + st);
+                const int c = k * (KIND == KIND_I8 ? kStepBytes : kStepBytes / 2);
+                mbar_arrive_expect_tx(full + st, kABytes + boxes * kBoxBytes);
+                copy_3d<1>(p, &a.tw, c, ch0, 0, fb);
+                for (int b = 0; b < boxes; ++b) copy_2d<1>(p + kABytes + b * kBoxBytes, &a.tx, c, row0 + b * kBoxRows, fb);
+                ++issued;
+                if (++st == a.stages) {
+                    st = 0;
+                    ph ^= 1;
+                }
+            }
+            for (int i = 0; !ok && i < a.stages && i < issued; ++i) {       // as in k_mma
+                const int m = issued - 1 - i;
+                const uint64_t t0 = global_timer_ns();
+                while (!mbar_try_wait_hint(full + m % a.stages, (uint32_t)(m / a.stages) & 1, 20000u) &&
+                       global_timer_ns() - t0 < kOpsDrainNs) {
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (elect_one()) {
+            int st = 0;
+            uint32_t ph = 0;
+            const uint32_t idesc = a.idesc | ((uint32_t)(n >> 3) << 17);
+            for (int k = k0; k < k1; ++k) {
+                if (!bar_wait(full + st, ph, abort_v)) break;
+                tc_after();
+                const uint32_t p = tiles0 + st * stage_bytes;
+                const uint64_t ad = sw128_desc(p), bd = sw128_desc(p + kABytes);
+                const int parts = min(4, (a.Kb - k * kStepBytes + 31) / 32);
+                if (parts == 4) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) umma<KIND, 1>(tmem, ad + 2 * i, bd + 2 * i, idesc, k > k0 || i > 0);
+                } else {
+                    for (int i = 0; i < parts; ++i) umma<KIND, 1>(tmem, ad + 2 * i, bd + 2 * i, idesc, k > k0 || i > 0);
+                }
+                umma_commit<1>(empty + st);
+                if (++st == a.stages) {
+                    st = 0;
+                    ph ^= 1;
+                }
+            }
+            umma_commit<1>(tfull);      // also after a wait that ran out: nothing may be in flight at the end
+        }
+    }
+    __syncwarp();
+    // Every warp waits for the MMAs (the ring is free then), eight of them move
+    // the accumulators: word (row, channel) at part[row * 128 + channel].
+    const bool done = __all_sync(0xffffffffu, bar_wait(tfull, 0, abort_v));
+    __syncthreads();                    // and no warp reads a barrier in the ring's way any more
+    tc_after();
+    uint32_t* part = reinterpret_cast<uint32_t*>(smem + (tiles0 - smem_addr(smem)));
+    if (warp >= 4 && done) {
+        const int q = warp & 3;
+        for (int c = ((warp - 4) >> 2) * 32; c < n; c += 64) {
+            uint32_t r[32];
+            tmem_read32(tmem + c + ((uint32_t)(q * 32) << 16), r);
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (c + j < rows) part[(c + j) * kTileCh + q * 32 + lane] = r[j];
+        }
+    }
+    __syncwarp();
+    tc_before();
+    cluster_sync();
+    tc_after();
+    if (warp == 2) tmem_free<1>(tmem, 256);
+    // this CTA's rows: a warp one row, a lane four channels
+    const int r0 = rows * rank / S, r1 = rows * (rank + 1) / S, ch = ch0 + 4 * lane;
+    float sw[4] = {1.0f, 1.0f, 1.0f, 1.0f}, bias[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (KIND == KIND_I8) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (ch + j < a.N) {
+                sw[j] = __ldg(a.sw + ch + j);
+                if (a.bias) bias[j] = __ldg(a.bias + ch + j);
+            }
+    }
+    const bool quad = a.ldy % 4 == 0 && ch + 4 <= a.N;
+    for (int r = r0 + warp; r < r1; r += kMmaThreads / 32) {
+        const uint32_t mine = smem_addr(part) + (r * kTileCh + 4 * lane) * 4;
+        uint4 w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            w[i] = make_uint4(0, 0, 0, 0);      // for codes a zero; fp32 partials past S are not added
+            if (i < S) {
+                uint32_t at;
+                asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(mine), "r"(i));
+                asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
+                             : "r"(at)
+                             : "memory");
+            }
+        }
+        float v[4];
+        if (KIND == KIND_I8) {
+            int t[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                t[0] += (int)w[i].x;
+                t[1] += (int)w[i].y;
+                t[2] += (int)w[i].z;
+                t[3] += (int)w[i].w;
+            }
+            const float sx = __ldg(a.sx + row0 + r);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v[j] = __fmul_rn(__fmul_rn((float)t[j], sw[j]), sx);
+                if (a.bias) v[j] = __fadd_rn(v[j], bias[j]);
+            }
+        } else {
+            v[0] = __uint_as_float(w[0].x);
+            v[1] = __uint_as_float(w[0].y);
+            v[2] = __uint_as_float(w[0].z);
+            v[3] = __uint_as_float(w[0].w);
+#pragma unroll
+            for (int i = 1; i < 8; ++i) {
+                if (i >= S) continue;
+                v[0] = __fadd_rn(v[0], __uint_as_float(w[i].x));
+                v[1] = __fadd_rn(v[1], __uint_as_float(w[i].y));
+                v[2] = __fadd_rn(v[2], __uint_as_float(w[i].z));
+                v[3] = __fadd_rn(v[3], __uint_as_float(w[i].w));
+            }
+        }
+        const int64_t at = (int64_t)(row0 + r) * a.ldy + ch;
+        if (quad) {
+            if (a.y_type == ELQ_F32)
+                *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.y) + at) = make_float4(v[0], v[1], v[2], v[3]);
+            else
+                *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.y) + at) =
+                    a.y_type == ELQ_BF16 ? make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]))
+                                         : make_uint2(pack_f16(v[0], v[1]), pack_f16(v[2], v[3]));
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (ch + j < a.N) store1(a.y, a.y_type, at + j, v[j]);
+        }
+    }
+    __syncwarp();
+    cluster_sync();         // no CTA leaves while another may still read its partials
 }
 
 }  // namespace elqops
