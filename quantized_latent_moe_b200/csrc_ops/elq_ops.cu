@@ -40,6 +40,9 @@ int device_sms() {
     return cache[dev];
 }
 
+// Every kernel here is launched so that it may start while the kernel before it on
+// the stream drains (programmatic dependent launch): it sets itself up, and waits
+// for that kernel's completion before it touches global memory.
 template <typename Args>
 cudaError_t launch(void (*kern)(Args), dim3 grid, dim3 threads, size_t smem, cudaStream_t s, const Args& a,
                    int cluster = 1) {
@@ -49,12 +52,14 @@ cudaError_t launch(void (*kern)(Args), dim3 grid, dim3 threads, size_t smem, cud
     cfg.blockDim = threads;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = cluster;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = cluster > 1 ? 1 : 0;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, a);
 }
 

@@ -192,6 +192,8 @@ __device__ __forceinline__ bool find_group(const int32_t* offsets, int E, int M,
 template <int KIND, int R>
 __global__ void __launch_bounds__(32 * kGemvWarps) k_gemv(const __grid_constant__ GemvArgs a) {
     const int n0 = (blockIdx.x * kGemvWarps + (threadIdx.x >> 5)) * R;
+    pdl_trigger();
+    pdl_wait();
     if (n0 >= a.N) return;
     for (int g = blockIdx.y;; g += gridDim.y) {
         int e = 0, r0 = 0, r1 = a.M;

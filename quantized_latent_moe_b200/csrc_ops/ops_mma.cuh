@@ -162,6 +162,10 @@ __device__ __forceinline__ void bar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+}
+
 // Tensor-map copies into this CTA's shared memory; `bar` is a cluster address, in
 // a pair of the first CTA's barrier.  No multicast.
 template <int CG>
@@ -352,6 +356,9 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_mma(const __grid_constant__ 
         fence_barrier_init();
     }
     if (warp == 2) tmem_alloc<CG>(s_tmem, 512);
+    if (warp == 3 && lane < 2) prefetch_map(lane ? &a.tx : &a.tw);
+    pdl_trigger();
+    pdl_wait();
     for (int i = threadIdx.x; i <= a.E; i += kMmaThreads)
         s_off[i] = a.offsets ? clamp_offset(__ldg(a.offsets + i), a.M) : (i ? a.M : 0);
     __syncthreads();
@@ -543,6 +550,9 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_split(const __grid_constant_
         fence_barrier_init();
     }
     if (warp == 2) tmem_alloc<1>(s_tmem, 256);
+    if (warp == 3 && lane < 2) prefetch_map(lane ? &a.tx : &a.tw);
+    pdl_trigger();
+    pdl_wait();
     __syncwarp();
     tc_before();
     __syncthreads();
