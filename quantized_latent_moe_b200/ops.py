@@ -173,31 +173,21 @@ def _experts(t, what, types, dev):
     return t.data_ptr(), ld if N > 1 else (K + 15) & ~15, st, E, N, K
 
 
-class _On:
-    """The device and stream of a call: ``with _On(device number, stream) as raw``."""
+# The current device's number, and the current stream of a device as an address: the getters under
+# torch.cuda.current_device() and torch.cuda.current_stream(), without the objects around them (4 us a call).
+_current = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
-    __slots__ = ("guard", "raw")
 
-    def __init__(self, dev, stream):
-        self.guard = None
-        if stream is not None:
-            if stream.device.index != dev:
-                _refuse("stream: of another device")
-            self.guard = torch.cuda.stream(stream)
-            self.raw = stream.cuda_stream
-        else:
-            if dev != torch.cuda.current_device():
-                self.guard = torch.cuda.device(dev)
-            self.raw = torch._C._cuda_getCurrentRawStream(dev)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self.raw
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _elsewhere(dev, stream, call, *args, **kw):
+    """The call again with its device and its stream (if one was given) current."""
+    if stream is None:
+        with torch.cuda.device(dev):
+            return call(*args, **kw)
+    if stream.device.index != dev:
+        _refuse("stream: of another device")
+    with torch.cuda.stream(stream):
+        return call(*args, **kw)
 
 
 def _ck(status, what):
@@ -233,9 +223,11 @@ def quantize_i8(x: torch.Tensor, index: torch.Tensor | None = None, index_div: i
     if index is not None:
         rows = index.numel()
         ip = _vector(index, rows, "quantize_i8: index", dev, torch.int32)
-    with _On(dev, stream) as s:
-        r, q, ldq, scale = I8Rows._new(x, rows, cols)
-        _ck(lib().elq_quantize_i8(p, ty, n, cols, ld, ip, index_div, rows, q, ldq, scale, s), "elq_quantize_i8")
+    if stream is not None or dev != _current():
+        return _elsewhere(dev, stream, quantize_i8, x, index, index_div)
+    r, q, ldq, scale = I8Rows._new(x, rows, cols)
+    _ck(lib().elq_quantize_i8(p, ty, n, cols, ld, ip, index_div, rows, q, ldq, scale, _raw_stream(dev)),
+        "elq_quantize_i8")
     return r
 
 
@@ -244,9 +236,11 @@ def swiglu_i8(gu: torch.Tensor, stream=None) -> I8Rows:
     p, ty, rows, cols, ld = _matrix(gu, "swiglu_i8: gu", FLOATS)
     if cols % 2:
         _refuse("swiglu_i8: an even number of columns")
-    with _On(gu.get_device(), stream) as s:
-        r, q, ldq, scale = I8Rows._new(gu, rows, cols // 2)
-        _ck(lib().elq_swiglu_i8(p, ty, rows, cols // 2, ld, q, ldq, scale, s), "elq_swiglu_i8")
+    dev = gu.get_device()
+    if stream is not None or dev != _current():
+        return _elsewhere(dev, stream, swiglu_i8, gu)
+    r, q, ldq, scale = I8Rows._new(gu, rows, cols // 2)
+    _ck(lib().elq_swiglu_i8(p, ty, rows, cols // 2, ld, q, ldq, scale, _raw_stream(dev)), "elq_swiglu_i8")
     return r
 
 
@@ -260,9 +254,10 @@ def combine_i8(o: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor, stream
     T, k = weights.shape
     wp = _vector(weights, T * k, "combine_i8: weights", dev)
     pp = _vector(pos, T * k, "combine_i8: pos", dev, torch.int32)
-    with _On(dev, stream) as s:
-        r, q, ldq, scale = I8Rows._new(o, T, cols)
-        _ck(lib().elq_combine_i8(p, ty, n, cols, ld, pp, wp, T, k, q, ldq, scale, s), "elq_combine_i8")
+    if stream is not None or dev != _current():
+        return _elsewhere(dev, stream, combine_i8, o, pos, weights)
+    r, q, ldq, scale = I8Rows._new(o, T, cols)
+    _ck(lib().elq_combine_i8(p, ty, n, cols, ld, pp, wp, T, k, q, ldq, scale, _raw_stream(dev)), "elq_combine_i8")
     return r
 
 
@@ -280,9 +275,10 @@ def i8_matmul(x: I8Rows, w: I8Rows, bias: torch.Tensor | None = None, out_dtype=
     if yt is None:
         _refuse("i8_matmul: out_dtype", UNSUPPORTED)
     bp = _vector(bias, N, "i8_matmul: bias", dev)
-    with _On(dev, stream) as s:
-        y, yp, ldy = _out(out, w._q if w._buf is None else w._buf, T, N, out_dtype, dev, "i8_matmul: out")
-        _ck(lib().elq_i8_matmul(xp, ldx, sx, T, wp, ldw, sw, bp, N, K, yp, yt, ldy, s), "elq_i8_matmul")
+    if stream is not None or dev != _current():
+        return _elsewhere(dev, stream, i8_matmul, x, w, bias, out_dtype, out)
+    y, yp, ldy = _out(out, w._q if w._buf is None else w._buf, T, N, out_dtype, dev, "i8_matmul: out")
+    _ck(lib().elq_i8_matmul(xp, ldx, sx, T, wp, ldw, sw, bp, N, K, yp, yt, ldy, _raw_stream(dev)), "elq_i8_matmul")
     return y
 
 
@@ -316,10 +312,11 @@ def grouped_matmul(x, w, offsets: torch.Tensor, out_dtype=None, out: torch.Tenso
     yt = FLOATS.get(out_dtype)
     if yt is None:
         _refuse("grouped_matmul: out_dtype", UNSUPPORTED)
-    with _On(dev, stream) as s:
-        y, yp, ldy = _out(out, wt, M, N, out_dtype, dev, "grouped_matmul: out")
-        _ck(lib().elq_grouped_matmul(xp, xt, ldx, sx, M, wp, ldw, st, sw, E, N, K, op, yp, yt, ldy, s),
-            "elq_grouped_matmul")
+    if stream is not None or dev != _current():
+        return _elsewhere(dev, stream, grouped_matmul, x, w, offsets, out_dtype, out)
+    y, yp, ldy = _out(out, wt, M, N, out_dtype, dev, "grouped_matmul: out")
+    _ck(lib().elq_grouped_matmul(xp, xt, ldx, sx, M, wp, ldw, st, sw, E, N, K, op, yp, yt, ldy, _raw_stream(dev)),
+        "elq_grouped_matmul")
     return y
 
 
@@ -337,9 +334,10 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float = 1
     nt = FLOATS.get(out_dtype)
     if nt is None:
         _refuse("rms_norm: out_dtype", UNSUPPORTED)
-    with _On(dev, stream) as s:
-        n, np, ldn = _out(out, x, T, C, out_dtype, dev, "rms_norm: out")
-        _ck(lib().elq_rms_norm(p, ty, T, C, ld, wp, eps, np, nt, ldn, None, s), "elq_rms_norm")
+    if stream is not None or dev != _current():
+        return _elsewhere(dev, stream, rms_norm, x, weight, eps, out_dtype, out)
+    n, np, ldn = _out(out, x, T, C, out_dtype, dev, "rms_norm: out")
+    _ck(lib().elq_rms_norm(p, ty, T, C, ld, wp, eps, np, nt, ldn, None, _raw_stream(dev)), "elq_rms_norm")
     return n
 
 
@@ -348,9 +346,10 @@ def rms_norm_i8(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float 
     p, ty, T, C, ld = _matrix(x, "rms_norm_i8: x", FLOATS)
     dev = x.get_device()
     wp = _vector(weight, C, "rms_norm_i8: weight", dev)
-    with _On(dev, stream) as s:
-        r, q, ldq, scale = I8Rows._new(x, T, C)
-        _ck(lib().elq_rms_norm(p, ty, T, C, ld, wp, eps, q, I8, ldq, scale, s), "elq_rms_norm")
+    if stream is not None or dev != _current():
+        return _elsewhere(dev, stream, rms_norm_i8, x, weight, eps)
+    r, q, ldq, scale = I8Rows._new(x, T, C)
+    _ck(lib().elq_rms_norm(p, ty, T, C, ld, wp, eps, q, I8, ldq, scale, _raw_stream(dev)), "elq_rms_norm")
     return r
 
 
@@ -386,28 +385,30 @@ def residual_norm(h: torch.Tensor, y: torch.Tensor, post_weight: torch.Tensor | 
             g_rows = max(T, 1) if G == 1 else 1
         if g_rows < 1 or G * g_rows < T:
             _refuse("residual_norm: gate rows")
-    with _On(dev, stream) as s:
-        h_out, op, ldo = _out(out, h, T, C, h.dtype, dev, "residual_norm: out")
-        n = nw = np = scale = None
-        nt = ldn = 0
-        if next_dtype is not None:
-            nw = _vector(next_weight, C, "residual_norm: next_weight", dev)
-            nt = TYPES.get(next_dtype)
-            if nt is None:
-                _refuse("residual_norm: next_dtype", UNSUPPORTED)
-            if nt == I8:
-                n, np, ldn, scale = I8Rows._new(h, T, C)
-            else:
-                n, np, ldn = _out(None, h, T, C, next_dtype, dev, "")
-        r = ResidualC(T, C, ht, yt, nt, hp, yp, pw, gp, nw, op, np, scale, ldh, ldy, ldo, ldn, g_rows, ldg, gc, res_scale,
-                      eps)
-        _ck(lib().elq_residual_norm(ctypes.byref(r), s), "elq_residual_norm")
+    if stream is not None or dev != _current():
+        return _elsewhere(dev, stream, residual_norm, h, y, post_weight, gate=gate, gate_rows=gate_rows,
+                          res_scale=res_scale, next_weight=next_weight, next_dtype=next_dtype, eps=eps, out=out)
+    h_out, op, ldo = _out(out, h, T, C, h.dtype, dev, "residual_norm: out")
+    n = nw = np = scale = None
+    nt = ldn = 0
+    if next_dtype is not None:
+        nw = _vector(next_weight, C, "residual_norm: next_weight", dev)
+        nt = TYPES.get(next_dtype)
+        if nt is None:
+            _refuse("residual_norm: next_dtype", UNSUPPORTED)
+        if nt == I8:
+            n, np, ldn, scale = I8Rows._new(h, T, C)
+        else:
+            n, np, ldn = _out(None, h, T, C, next_dtype, dev, "")
+    r = ResidualC(T, C, ht, yt, nt, hp, yp, pw, gp, nw, op, np, scale, ldh, ldy, ldo, ldn, g_rows, ldg, gc, res_scale, eps)
+    _ck(lib().elq_residual_norm(ctypes.byref(r), _raw_stream(dev)), "elq_residual_norm")
     return h_out, n
 
 
 def status(device=None, stream=None) -> int:
     """Blocking: whether a product's bounded device wait ran out since the last
     call (0, or the timeout status)."""
-    dev = torch.cuda.current_device() if device is None else torch.device(device).index
-    with _On(dev, stream) as s:
-        return int(lib().elq_ops_status(s))
+    dev = torch.cuda.current_device() if device is None else torch.cuda.device(device).idx
+    if stream is not None or dev != _current():
+        return _elsewhere(dev, stream, status, dev)
+    return int(lib().elq_ops_status(_raw_stream(dev)))
