@@ -222,11 +222,8 @@ struct Product {
     int kind;
 };
 
-constexpr int kGemvMaxRows = 8;
-
-template <int KIND>
+template <int KIND, int R, int U>
 cudaError_t launch_gemv(const Product& p, cudaStream_t s) {
-    constexpr int R = 2;
     const int es = KIND == KIND_I8 ? 1 : 2;
     GemvArgs a;
     a.x = (const uint8_t*)p.x;
@@ -246,8 +243,24 @@ cudaError_t launch_gemv(const Product& p, cudaStream_t s) {
     a.y_type = p.y_type;
     a.ldy = p.ldy;
     const int per = kGemvWarps * R;
-    const dim3 grid((unsigned)(((int64_t)p.N + per - 1) / per), p.offsets ? std::min(p.E, p.M) : 1);
-    return launch(k_gemv<KIND, R>, grid, 32 * kGemvWarps, 0, s, a);
+    // four CTAs an SM, each going on to further channels: what a CTA does before its
+    // first weights arrive (finding its group) is done once for all of them
+    const int groups = p.offsets ? std::min(p.E, p.M) : 1;
+    const int most = std::max(1, 4 * device_sms() / groups);
+    const dim3 grid((unsigned)std::min<int64_t>(most, ((int64_t)p.N + per - 1) / per), groups);
+    return launch(k_gemv<KIND, R, U>, grid, 32 * kGemvWarps, 0, s, a);
+}
+
+// Channels a warp takes at a time (R) and pieces of each in flight (U).  8-bit
+// codes: four channels, two pieces, where that leaves work for every warp (8 rows
+// of 8 experts of 2048 x 1792: 7.8 us, 9.0 with two and four; tensor cores 9.2);
+// else two and four (1 row 4096 -> 1792: 4.4 us, 5.3 with four and two).  16-bit:
+// two and four, since each weight is widened into registers.
+cudaError_t launch_gemv(const Product& p, cudaStream_t s) {
+    if (p.kind == KIND_BF16) return launch_gemv<KIND_BF16, 2, 4>(p, s);
+    if (p.kind == KIND_F16) return launch_gemv<KIND_F16, 2, 4>(p, s);
+    const int64_t channels = (int64_t)p.N * (p.offsets ? std::min(p.E, p.M) : 1);
+    return channels >= 40 * device_sms() ? launch_gemv<KIND_I8, 4, 2>(p, s) : launch_gemv<KIND_I8, 2, 4>(p, s);
 }
 
 // Row tiles, in whole copied boxes of 32 rows a CTA: as many rows as the group can have up to 256; a dense product takes
@@ -381,12 +394,17 @@ elq_status launch_mma(const Product& p, cudaStream_t s) {
     return pairs * row_tiles > device_sms() / 2 ? launch_mma<KIND, 2>(p, s) : launch_mma<KIND, 1>(p, s);
 }
 
+// The register GEMV for grouped products of up to 8 rows (above, the tensor cores
+// read the weights faster: 16 rows of 16 experts); dense ones of up to 4, or 8 of a
+// matrix below 1 MB (6 rows 4096 -> 1792: 6.2 us against 5.5 split over K; 512 ->
+// 512: 1.9 against 4.2).
+bool few_rows(const Product& p) {
+    if (p.offsets || p.M <= 4) return p.M <= 8;
+    return p.M <= 8 && (int64_t)p.N * p.K * (p.kind == KIND_I8 ? 1 : 2) <= 1 << 20;
+}
+
 elq_status run_product(const Product& p, cudaStream_t s) {
-    if (p.M <= kGemvMaxRows) {
-        return status_of(p.kind == KIND_I8     ? launch_gemv<KIND_I8>(p, s)
-                         : p.kind == KIND_BF16 ? launch_gemv<KIND_BF16>(p, s)
-                                               : launch_gemv<KIND_F16>(p, s));
-    }
+    if (few_rows(p)) return status_of(launch_gemv(p, s));
     return p.kind == KIND_I8 ? launch_mma<KIND_I8>(p, s) : p.kind == KIND_BF16 ? launch_mma<KIND_BF16>(p, s)
                                                                                : launch_mma<KIND_F16>(p, s);
 }

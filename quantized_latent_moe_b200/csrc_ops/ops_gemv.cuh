@@ -1,5 +1,5 @@
 // ops_gemv.cuh -- products for a few rows: every weight is read once, straight
-// from HBM into registers, and multiplied with up to eight rows of activations
+// from HBM into registers, and multiplied with up to four rows of activations
 // that come from L1.
 //
 // A warp owns R neighbouring output channels over all of K: lane i takes the
@@ -100,10 +100,9 @@ __device__ __forceinline__ void gemv_piece(const uint4 (&w)[R], const uint4 (&x)
 }
 
 // Channels n0 .. n0+R-1 of expert matrix w times rows t0 .. t0+nt-1 (nt <= TB).
-template <int KIND, int R, int TB>
+template <int KIND, int R, int TB, int U>
 __device__ __forceinline__ void gemv_rows(const GemvArgs& a, const uint8_t* w, const float* sw, int n0, int t0, int nt) {
     using Acc = typename std::conditional<KIND == KIND_I8, int, float>::type;
-    constexpr int U = TB <= 2 ? 4 : 2;      // pieces of each channel in flight
     constexpr int C = R * TB;
     const int lane = threadIdx.x & 31;
     const uint8_t* wr[R];
@@ -189,12 +188,10 @@ __device__ __forceinline__ bool find_group(const int32_t* offsets, int E, int M,
     return false;
 }
 
-template <int KIND, int R>
+template <int KIND, int R, int U>
 __global__ void __launch_bounds__(32 * kGemvWarps) k_gemv(const __grid_constant__ GemvArgs a) {
-    const int n0 = (blockIdx.x * kGemvWarps + (threadIdx.x >> 5)) * R;
     pdl_trigger();
     pdl_wait();
-    if (n0 >= a.N) return;
     for (int g = blockIdx.y;; g += gridDim.y) {
         int e = 0, r0 = 0, r1 = a.M;
         if (a.offsets) {
@@ -204,12 +201,13 @@ __global__ void __launch_bounds__(32 * kGemvWarps) k_gemv(const __grid_constant_
         }
         const uint8_t* w = a.w + (int64_t)e * a.w_stride;
         const float* sw = KIND == KIND_I8 ? a.sw + (int64_t)e * a.N : nullptr;
-        for (int t0 = r0; t0 < r1; t0 += 8) {
-            const int nt = min(8, r1 - t0);
-            if (nt == 1) gemv_rows<KIND, R, 1>(a, w, sw, n0, t0, nt);
-            else if (nt == 2) gemv_rows<KIND, R, 2>(a, w, sw, n0, t0, nt);
-            else if (nt <= 4) gemv_rows<KIND, R, 4>(a, w, sw, n0, t0, nt);
-            else gemv_rows<KIND, R, 8>(a, w, sw, n0, t0, nt);
+        for (int n0 = (blockIdx.x * kGemvWarps + (threadIdx.x >> 5)) * R; n0 < a.N; n0 += gridDim.x * kGemvWarps * R) {
+            for (int t0 = r0; t0 < r1; t0 += 4) {
+                const int nt = min(4, r1 - t0);
+                if (nt == 1) gemv_rows<KIND, R, 1, U>(a, w, sw, n0, t0, nt);
+                else if (nt == 2) gemv_rows<KIND, R, 2, U>(a, w, sw, n0, t0, nt);
+                else gemv_rows<KIND, R, 4, U>(a, w, sw, n0, t0, nt);
+            }
         }
     }
 }
