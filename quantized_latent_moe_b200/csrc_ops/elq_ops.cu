@@ -75,6 +75,10 @@ cudaError_t launch_pipe_t(const RowArgs& a, int threads, int groups, size_t smem
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kMaxDevices || !optin[dev]) {
         e = cudaFuncSetAttribute(k_pipe<OP, VPT, D, XT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPipeSmem);
+        // all of the SM's memory as shared memory: by itself the driver gave four CTAs' worth
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(k_pipe<OP, VPT, D, XT>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                     cudaSharedmemCarveoutMaxShared);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < kMaxDevices) optin[dev] = true;
     }

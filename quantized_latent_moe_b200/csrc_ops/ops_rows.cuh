@@ -211,10 +211,14 @@ __device__ __forceinline__ uint2 codes8(const float (&v)[8], const CodeScale& c)
 // enough; words of absent warps are zero.
 constexpr int kRowGroups = 8;           // most rows of a CTA at a time
 
+// GROUPS: blockDim.y may be above 1, and each row has a named barrier of its own.
+// (A barrier named at run time makes a CTA hold all sixteen, of which an SM has 64:
+// kernels without groups use the CTA's.)
+template <bool GROUPS>
 struct RowReduce {
     uint32_t (*red)[16];
     int turn;
-    __device__ __forceinline__ RowReduce(uint32_t (*r)[16]) : red(r + 2 * threadIdx.y), turn(0) {
+    __device__ __forceinline__ RowReduce(uint32_t (*r)[16]) : red(r + (GROUPS ? 2 * threadIdx.y : 0)), turn(0) {
         if (threadIdx.x < 32) red[threadIdx.x >> 4][threadIdx.x & 15] = 0;
         __syncthreads();
     }
@@ -222,7 +226,8 @@ struct RowReduce {
         uint32_t* r = red[turn];
         turn ^= 1;
         if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = v;
-        asm volatile("bar.sync %0, %1;" ::"r"(threadIdx.y + 1), "r"(blockDim.x) : "memory");
+        if (GROUPS) asm volatile("bar.sync %0, %1;" ::"r"(threadIdx.y + 1), "r"(blockDim.x) : "memory");
+        else __syncthreads();
         return reinterpret_cast<const uint4*>(r);
     }
     __device__ __forceinline__ float sum(float v) {
@@ -457,7 +462,7 @@ template <int OP, int VPT, bool VEC>
 __global__ void __launch_bounds__(kRowThreads) k_rows(const __grid_constant__ RowArgs a) {
     __shared__ __align__(16) uint32_t red[2][16];
     pdl_trigger();
-    RowReduce rr(red);
+    RowReduce<false> rr(red);
     pdl_wait();
     const int nch = (int)((a.cols + 8ll * blockDim.x - 1) / (8ll * blockDim.x));      // chunks of a thread
     constexpr int NV = VPT > 0 ? VPT : 1;
@@ -735,7 +740,7 @@ __global__ void __launch_bounds__(VPT == 1 ? kRowThreads : kPipeThreads4, 2) k_p
     }
     if ((OP == ROW_RMS || OP == ROW_RESIDUAL) && blockDim.y > 1)        // the other rows' threads read the weights too
         asm volatile("cp.async.wait_group 0;" ::: "memory");
-    RowReduce rr(red);                                                  // a barrier of the CTA
+    RowReduce<OP == ROW_RMS || OP == ROW_RESIDUAL> rr(red);             // a barrier of the CTA
 
     for (int st = 0; row < a.rows; row += step, st = st + 1 == D ? 0 : st + 1) {
         fetch(ring + (st == 0 ? D - 1 : st - 1) * stage_bytes, row + (D - 1) * step, ahead);
