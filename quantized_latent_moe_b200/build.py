@@ -1,16 +1,21 @@
-"""Build libelq.so (the C ABI of include/elq.h) in-tree with nvcc for sm_100a."""
+"""Build libelq.so (the C ABI of include/elq.h and include/elq_ops.h) in-tree with nvcc for
+sm_100a, and _ops.so, the compiled Python binding of the latter, with the host compiler."""
 from __future__ import annotations
 
 import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = [os.path.join(HERE, d) for d in ("csrc", "csrc_ops")]
 OBJ = os.path.join(HERE, "_build")          # one object per source, rebuilt when stale
 LIB = os.path.join(HERE, "libelq.so")
+BINDING = os.path.join(HERE, "_ops.so")
+BINDING_SRC = os.path.join(CSRC[1], "ops_binding.cpp")
+CXX = os.environ.get("CXX", "g++")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 FLAGS = [
@@ -44,32 +49,50 @@ def _run(cmds):
     outs = [p.communicate()[0] for p in procs]
     if any(p.returncode for p in procs):
         sys.stderr.write("".join(outs))
-        raise RuntimeError("nvcc failed building libelq.so")
+        raise RuntimeError("the compiler failed building libelq.so or _ops.so")
     return "".join(outs)
 
 
+def _stale(target, sources):
+    return not os.path.exists(target) or os.path.getmtime(target) < max(os.path.getmtime(p) for p in sources)
+
+
+def _binding_cmd(out):
+    import torch
+    root = os.path.dirname(torch.__file__)
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include")]
+    return [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
+            *["-I" + p for p in inc], BINDING_SRC, "-o", out, "-L" + HERE, "-l:libelq.so",
+            "-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_python",
+            "-Wl,-rpath,$ORIGIN"]
+
+
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
-    newest = max(os.path.getmtime(p) for p in deps())
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= newest:
-        return LIB
-    os.makedirs(OBJ, exist_ok=True)
-    cmds, objs, done = [], [], []
-    for src in sources():
-        obj = os.path.join(OBJ, os.path.basename(src) + ".o")
-        objs.append(obj)
-        if force or extra or not os.path.exists(obj) or os.path.getmtime(obj) < max(
-                os.path.getmtime(p) for p in [src] + headers(src)):
-            tmp = obj + ".tmp%d" % os.getpid()
-            cmds.append([NVCC, *(["-Xptxas=-v"] if verbose else []), *FLAGS, *extra, "-c", "-o", tmp, src])
-            done.append((tmp, obj))
-    out = _run(cmds)
-    for tmp, obj in done:
-        os.replace(tmp, obj)
-    tmp = LIB + ".tmp%d" % os.getpid()
-    out += _run([[NVCC, *FLAGS, "-shared", "-o", tmp, *objs]])
+    out = ""
+    if force or extra or _stale(LIB, deps()):
+        os.makedirs(OBJ, exist_ok=True)
+        cmds, objs, done = [], [], []
+        for src in sources():
+            obj = os.path.join(OBJ, os.path.basename(src) + ".o")
+            objs.append(obj)
+            if force or extra or _stale(obj, [src] + headers(src)):
+                tmp = obj + ".tmp%d" % os.getpid()
+                cmds.append([NVCC, *(["-Xptxas=-v"] if verbose else []), *FLAGS, *extra, "-c", "-o", tmp, src])
+                done.append((tmp, obj))
+        out = _run(cmds)
+        for tmp, obj in done:
+            os.replace(tmp, obj)
+        tmp = LIB + ".tmp%d" % os.getpid()
+        out += _run([[NVCC, *FLAGS, "-shared", "-o", tmp, *objs]])
+        os.replace(tmp, LIB)
+    if force or _stale(BINDING, [BINDING_SRC, os.path.join(ROOT, "include", "elq.h"),
+                                 os.path.join(ROOT, "include", "elq_ops.h"), __file__]):
+        tmp = BINDING + ".tmp%d" % os.getpid()
+        out += _run([_binding_cmd(tmp)])
+        os.replace(tmp, BINDING)
     if verbose:
         sys.stderr.write(out)
-    os.replace(tmp, LIB)
     return LIB
 
 
