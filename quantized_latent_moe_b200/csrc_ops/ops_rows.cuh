@@ -129,6 +129,42 @@ __device__ __forceinline__ void store8(void* p, int type, int64_t i, const float
         *d = make_uint4(pack_f16(v[0], v[1]), pack_f16(v[2], v[3]), pack_f16(v[4], v[5]), pack_f16(v[6], v[7]));
 }
 
+// Pairs of fp32 values in one 64-bit register, and the packed operations on them:
+// each half is one IEEE round-to-nearest operation, at half the instructions.
+typedef unsigned long long f32x2;
+
+__device__ __forceinline__ f32x2 pair(float lo, float hi) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 halves(f32x2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 sub2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+// The largest of three magnitudes, a NaN if one is a NaN.
+__device__ __forceinline__ float max_abs3(float a, float b, float c) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // The scale of a row and what its codes need: x / s to the nearest whole
 // number, exactly.  q = rint(x * inv) is within one of it; the remainder
 // r = x - q * s is exact in fp32 (one fused multiply-add), and its comparison
@@ -176,33 +212,45 @@ __device__ __forceinline__ int code_of(float x, const CodeScale& c) {
 // compared with half a scale all eight at once, and only eight that have one at
 // or past it are settled one by one.  (bf16 rows have such border cases: half of
 // a row's largest value is 63.5 scales, and about one value in a thousand is it.)
-__device__ __forceinline__ uint2 codes8(const float (&v)[8], const CodeScale& c) {
+__device__ __forceinline__ uint2 codes8(const f32x2 (&v)[4], const CodeScale& c) {
     if (c.inv == 0.0f) return make_uint2(0, 0);
     uint32_t b[8];
     if (c.up == 1.0f) {
+        const f32x2 magic = pair(12582912.0f, 12582912.0f), inv = pair(c.inv, c.inv), sm = pair(c.sm, c.sm);
         float worst = 0.0f;
+        f32x2 r[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float t = __fmaf_rn(v[j], c.inv, 12582912.0f);
-            b[j] = __float_as_uint(t);
-            worst = fmaxf(worst, fabsf(__fmaf_rn(-__fsub_rn(t, 12582912.0f), c.sm, v[j])));
+        for (int j = 0; j < 4; ++j) {
+            const f32x2 t = fma2(v[j], inv, magic);
+            const float2 h = halves(t);
+            b[2 * j] = __float_as_uint(h.x);
+            b[2 * j + 1] = __float_as_uint(h.y);
+            r[j] = fma2(sub2(magic, t), sm, v[j]);      // v - q * s
+            const float2 e = halves(r[j]);
+            worst = max_abs3(worst, e.x, e.y);
         }
         if (worst >= c.half) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float r = __fmaf_rn(-__fsub_rn(__uint_as_float(b[j]), 12582912.0f), c.sm, v[j]);
-                const float away = __uint_as_float(__float_as_uint(r) ^ (__float_as_uint(v[j]) & 0x80000000u));
-                const uint32_t one = v[j] < 0.0f ? ~0u : 1u;
+                const float x = j & 1 ? halves(v[j >> 1]).y : halves(v[j >> 1]).x;
+                const float e = j & 1 ? halves(r[j >> 1]).y : halves(r[j >> 1]).x;
+                const float away = __uint_as_float(__float_as_uint(e) ^ (__float_as_uint(x) & 0x80000000u));
+                const uint32_t one = x < 0.0f ? ~0u : 1u;
                 if (away >= c.half) b[j] += one;
                 else if (away < -c.half) b[j] -= one;
             }
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) b[j] = (uint32_t)code_of(v[j], c);
+        for (int j = 0; j < 8; ++j) b[j] = (uint32_t)code_of(j & 1 ? halves(v[j >> 1]).y : halves(v[j >> 1]).x, c);
     }
     return make_uint2(__byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410),
                       __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410));
+}
+
+__device__ __forceinline__ void pairs8(const float (&v)[8], f32x2 (&p)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) p[j] = pair(v[2 * j], v[2 * j + 1]);
 }
 
 // Reductions over the threads of a row (blockDim.x, up to 16 warps; a CTA has
@@ -316,7 +364,9 @@ template <bool VEC>
 __device__ __forceinline__ void put_codes8(int8_t* q, int64_t row0, int i, int cols, const float (&v)[8],
                                            const CodeScale& cs) {
     if (VEC && elem<VEC>(i, 0) + 8 <= cols) {
-        *reinterpret_cast<uint2*>(q + row0 + elem<VEC>(i, 0)) = codes8(v, cs);
+        f32x2 p[4];
+        pairs8(v, p);
+        *reinterpret_cast<uint2*>(q + row0 + elem<VEC>(i, 0)) = codes8(p, cs);
         return;
     }
 #pragma unroll
@@ -326,10 +376,15 @@ __device__ __forceinline__ void put_codes8(int8_t* q, int64_t row0, int i, int c
     }
 }
 
-// The larger of m and |v|, a NaN if either is one.
+// The largest of m and the values' magnitudes, a NaN if there is one.
 __device__ __forceinline__ float amax8(float m, const float (&v)[8]) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(v[j])));
+    for (int j = 0; j < 8; j += 2) m = max_abs3(m, v[j], v[j + 1]);
+    return m;
+}
+__device__ __forceinline__ float amax8(float m, const f32x2 (&v)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m = max_abs3(m, halves(v[j]).x, halves(v[j]).y);
     return m;
 }
 
@@ -349,16 +404,23 @@ __device__ __forceinline__ float rstd_of(float ss, float inv_cols, float eps) {
 // exp(-g) = 2^n * 2^f with n whole and f reduced by a two-part log2(e); the
 // hardware's 2^f is good to 2^-22 and its reciprocal to 2^-23, both far below the
 // half step of the code that follows.
-__device__ __forceinline__ float swiglu1(float g, float u) {
-    const float z = fminf(fmaxf(-g, -87.0f), 88.0f);
-    const float n = rintf(__fmul_rn(z, 1.44269502f));
-    float f = __fmaf_rn(z, 1.44269502f, -n);
-    f = __fmaf_rn(z, 1.92596299e-8f, f);
-    float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(f));
-    e = __fmul_rn(e, __int_as_float(((int)n + 127) << 23));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(__fadd_rn(1.0f, e)));
-    return __fmul_rn(__fmul_rn(g, r), u);
+__device__ __forceinline__ f32x2 swiglu2(f32x2 g, f32x2 u) {
+    const float2 h = halves(g);
+    const f32x2 magic = pair(12582912.0f, 12582912.0f), l = pair(1.44269502f, 1.44269502f);
+    const f32x2 z = pair(fminf(fmaxf(-h.x, -87.0f), 88.0f), fminf(fmaxf(-h.y, -87.0f), 88.0f));
+    const f32x2 t = fma2(z, l, magic);                          // n, in the low bits
+    const f32x2 n = sub2(magic, t);                             // -n
+    f32x2 f = fma2(z, l, n);
+    f = fma2(z, pair(1.92596299e-8f, 1.92596299e-8f), f);
+    float e[2] = {halves(f).x, halves(f).y};
+    const uint32_t nb[2] = {__float_as_uint(halves(t).x), __float_as_uint(halves(t).y)};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e[i]) : "f"(e[i]));
+        e[i] = __fadd_rn(1.0f, __uint_as_float(__float_as_uint(e[i]) + (nb[i] << 23)));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(e[i]) : "f"(e[i]));
+    }
+    return mul2(mul2(g, pair(e[0], e[1])), u);
 }
 
 // The eight source values of chunk ci of output row `row` (the quantisers'
@@ -377,8 +439,10 @@ __device__ __forceinline__ void source8(const RowArgs& a, int64_t row, int64_t s
         get8<VEC>(a.x, a.x_type, row * a.ldx, ci, a.cols, v);
         get8<VEC>(a.x, a.x_type, row * a.ldx + a.cols, ci, a.cols, u);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            v[j] = swiglu1(v[j], u[j]);
+        for (int j = 0; j < 8; j += 2) {
+            const float2 h = halves(swiglu2(pair(v[j], v[j + 1]), pair(u[j], u[j + 1])));
+            v[j] = h.x;
+            v[j + 1] = h.y;
         }
     } else if (OP == ROW_COMBINE) {
 #pragma unroll
@@ -599,6 +663,10 @@ __device__ __forceinline__ uint4 lds16(uint32_t a) {
     return r;
 }
 
+__device__ __forceinline__ void lds_pairs(uint32_t a, f32x2& x, f32x2& y) {
+    asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(x), "=l"(y) : "r"(a));
+}
+
 // The pieces of a row, in order: x's (SwiGLU: the gate's, then the up's), h's,
 // a gate that changes from row to row; and of the weights: the written norm's, and
 // the product of the post-norm's and a gate that all rows share.  Every fp32 chunk
@@ -627,18 +695,20 @@ struct Lane {
             for (int i = 0; i < VPT; ++i) copy16(at + i * row_bytes16, src + (int64_t)i * row_bytes16, on * 2 * nv[i]);
         }
     }
-    __device__ __forceinline__ void read(uint32_t at, int i, int type, float (&v)[8]) const {
+    __device__ __forceinline__ void read(uint32_t at, int i, int type, f32x2 (&v)[4]) const {
         if (type == ELQ_F32) {
-            const uint4 a = lds16(at + (2 * i) * row_bytes16), b = lds16(at + (2 * i + 1) * row_bytes16);
-            const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(w[j]);
+            lds_pairs(at + (2 * i) * row_bytes16, v[0], v[1]);
+            lds_pairs(at + (2 * i + 1) * row_bytes16, v[2], v[3]);
         } else {
-            widen8(lds16(at + i * row_bytes16), type, v);
+            float w[8];
+            widen8(lds16(at + i * row_bytes16), type, w);
+            pairs8(w, v);
         }
     }
     // v to a row at dst (its first value), rounded to type
-    __device__ __forceinline__ void write(uint8_t* dst, int i, int type, const float (&v)[8]) const {
+    __device__ __forceinline__ void write(uint8_t* dst, int i, int type, const f32x2 (&p)[4]) const {
+        const float v[8] = {halves(p[0]).x, halves(p[0]).y, halves(p[1]).x, halves(p[1]).y,
+                            halves(p[2]).x, halves(p[2]).y, halves(p[3]).x, halves(p[3]).y};
         if (nv[i] == 8) {
             if (type == ELQ_F32) store8(dst + threadIdx.x * 32 + (int64_t)(2 * i) * row_bytes16, type, 0, v);
             else store8(dst + threadIdx.x * 16 + (int64_t)i * row_bytes16, type, 0, v);
@@ -649,7 +719,7 @@ struct Lane {
                 if (j < nv[i]) store1(dst, type, e0 + j, v[j]);
         }
     }
-    __device__ __forceinline__ void write_codes(int8_t* dst, int i, const float (&v)[8], const CodeScale& cs) const {
+    __device__ __forceinline__ void write_codes(int8_t* dst, int i, const f32x2 (&v)[4], const CodeScale& cs) const {
         const int e0 = 8 * threadIdx.x + i * (row_bytes16 >> 1);
         const uint2 w = codes8(v, cs);
         if (nv[i] == 8) {
@@ -661,6 +731,18 @@ struct Lane {
         }
     }
 };
+
+// The sum of squares of a thread's values.
+template <int VPT>
+__device__ __forceinline__ float sumsq(const f32x2 (&v)[VPT][4]) {
+    f32x2 s = 0;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s = fma2(v[i][j], v[i][j], s);
+    const float2 h = halves(s);
+    return __fadd_rn(h.x, h.y);
+}
 
 // A CTA works on blockDim.y rows at a time, blockDim.x threads each, which share
 // the weights in shared memory.  D stages: the rows in shared memory per row
@@ -747,65 +829,59 @@ __global__ void __launch_bounds__(VPT == 1 ? kRowThreads : kPipeThreads4, 2) k_p
         ahead = source(row + D * step);
         asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
         const uint32_t at = ring + st * stage_bytes;
-        float v[VPT][8];
+        f32x2 v[VPT][4];
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             ln.read(at, i, xt, v[i]);
             if (OP == ROW_SWIGLU) {
-                float u[8];
+                f32x2 u[4];
                 ln.read(at + ox, i, xt, u);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[i][j] = swiglu1(v[i][j], u[j]);
+                for (int j = 0; j < 4; ++j) v[i][j] = swiglu2(v[i][j], u[j]);
             }
         }
         if constexpr (OP == ROW_RESIDUAL) {
-            float ss = 0.0f;
-#pragma unroll
-            for (int i = 0; i < VPT; ++i) ss = sumsq8(ss, v[i]);
-            const float rstd = rstd_of(rr.sum(ss), a.inv_cols, a.eps);
+            const float rstd = rstd_of(rr.sum(sumsq(v)), a.inv_cols, a.eps);
             const float g0 = a.gate && a.gate_cols == 1 ? a.gate[(row / a.gate_rows) * a.gate_ld] : 1.0f;
             uint8_t* o = op + row * bo;
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
-                float h[8], w[8];
+                f32x2 h[4], w[4];
                 // past the row's end y and h are 0, and so is h'
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[i][j] = __fmul_rn(v[i][j], rstd);
+                for (int j = 0; j < 4; ++j) v[i][j] = mul2(v[i][j], pair(rstd, rstd));
                 if (wg) {
                     ln.read(w_first, i, ELQ_F32, w);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) v[i][j] = __fmul_rn(v[i][j], w[j]);
+                    for (int j = 0; j < 4; ++j) v[i][j] = mul2(v[i][j], w[j]);
                 }
                 ln.read(at + oh, i, ht, h);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) h[j] = __fmul_rn(a.res_scale, h[j]);
+                for (int j = 0; j < 4; ++j) h[j] = mul2(pair(a.res_scale, a.res_scale), h[j]);
                 if (gate_row) {
                     ln.read(at + og, i, ELQ_F32, w);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) v[i][j] = __fmaf_rn(w[j], v[i][j], h[j]);
+                    for (int j = 0; j < 4; ++j) v[i][j] = fma2(w[j], v[i][j], h[j]);
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) v[i][j] = __fmaf_rn(g0, v[i][j], h[j]);
+                    for (int j = 0; j < 4; ++j) v[i][j] = fma2(pair(g0, g0), v[i][j], h[j]);
                 }
                 ln.write(o, i, ht, v[i]);
             }
             if (!a.n) continue;
         }
         if constexpr (OP == ROW_RMS || OP == ROW_RESIDUAL) {
-            float ss = 0.0f;
-#pragma unroll
-            for (int i = 0; i < VPT; ++i) ss = sumsq8(ss, v[i]);
-            const float rstd = rstd_of(rr.sum(ss), a.inv_cols, a.eps);
+            const float rstd = rstd_of(rr.sum(sumsq(v)), a.inv_cols, a.eps);
             uint8_t* o = np + row * bn;
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[i][j] = __fmul_rn(v[i][j], rstd);
+                for (int j = 0; j < 4; ++j) v[i][j] = mul2(v[i][j], pair(rstd, rstd));
                 if (w_last) {
-                    float w[8];
+                    f32x2 w[4];
                     ln.read(ln.first, i, ELQ_F32, w);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) v[i][j] = __fmul_rn(v[i][j], w[j]);
+                    for (int j = 0; j < 4; ++j) v[i][j] = mul2(v[i][j], w[j]);
                 }
                 if (!codes) ln.write(o, i, a.n_type, v[i]);
             }
