@@ -22,6 +22,7 @@
  *  - Types: ELQ_F32, ELQ_BF16, ELQ_F16 and, where said, ELQ_I8.
  *  - Sums, norms and softmax weights are fp32, integer sums int32; each output
  *    is rounded once, to nearest even, to its type.
+ *  - Rows, channels and columns number at most 2^30 each.
  *  - No workspace, no allocation, nothing kept between calls but what elq.h
  *    names; any stream, capturable; calls do not share anything on the GPU.
  *    An output may not overlap an input, except where in-place use is said.
@@ -57,7 +58,7 @@ enum {                          /* more GGUF type ids */
  * index[i] / div (index: device int32 [rows]; e.g. the pair order perm of
  * elq_route_bucket with div = k), or source row i where index is NULL (then
  * div is 1 and rows <= x_rows).  An index that is negative or names a row past
- * x_rows gives a zero row.  x: device [x_rows][cols], x_type F32, BF16 or F16,
+ * x_rows (>= 1) gives a zero row.  x: device [x_rows][cols], x_type F32, BF16 or F16,
  * leading dimension ldx.  q: device int8 [rows][cols], ldq a multiple of 16;
  * scale: device fp32 [rows].  Also gives a weight matrix [N][K] its codes and
  * per-channel scales. */
@@ -75,7 +76,7 @@ elq_status elq_swiglu_i8(const void* gu, int32_t x_type, int64_t rows, int32_t I
  * of weights[t][j] * o[pos[t][j]] in fp32 (fused multiply-adds from 0),
  * quantised to q [T][cols] and scale [T].  o: device [o_rows][cols], o_type F32,
  * BF16 or F16; pos: device int32 [T][k] (elq_route_bucket's); weights: device
- * fp32 [T][k]; k <= 64.  A position outside 0 .. o_rows-1 adds nothing. */
+ * fp32 [T][k]; k <= 64.  A position outside 0 .. o_rows-1 adds nothing (o_rows >= 1). */
 elq_status elq_combine_i8(const void* o, int32_t o_type, int64_t o_rows, int32_t cols, int64_t ldo,
                           const int32_t* pos, const float* weights, int64_t T, int32_t k, int8_t* q,
                           int64_t ldq, float* scale, void* stream);
@@ -97,12 +98,11 @@ elq_status elq_i8_matmul(const int8_t* x, int64_t ldx, const float* sx, int64_t 
  * (elements, >= (N-1) * ldw + K) between experts; both x_type: I8 (with sx [M]
  * and sw [E][N]), BF16 or F16 (sx and sw NULL; fp32 accumulation).  y: device
  * [M][N], y_type F32 or, for I8, BF16 or F16; for 16-bit x F32 or x_type.
- * offsets: device int32 [E+1], non-decreasing, as elq_route_bucket writes them;
- * each is clamped to 0 .. M and a group whose end lies before its start is
- * empty.  Rows outside every group are left as they were; where offsets are not
- * non-decreasing, each value of a row in two groups is one of their products.  Row lengths of x
- * and w whole multiples of 16 bytes apart (ldx, ldw, w_stride); 1 <= K <= 65536,
- * N >= 1, 1 <= E <= 1024, M < 2^31. */
+ * offsets: device int32 [E+1], non-decreasing, as elq_route_bucket writes them
+ * (each is taken as clamped to 0 .. M and raised to the largest before it, so
+ * that groups are disjoint whatever the array holds).  Rows outside every group
+ * are left as they were.  Rows of x and w and experts of w are whole multiples of
+ * 16 bytes apart (ldx, ldw, w_stride); 1 <= K <= 65536, 1 <= E <= 1024. */
 elq_status elq_grouped_matmul(const void* x, int32_t x_type, int64_t ldx, const float* sx, int64_t M, const void* w,
                               int64_t ldw, int64_t w_stride, const float* sw, int32_t E, int32_t N, int32_t K,
                               const int32_t* offsets, void* y, int32_t y_type, int64_t ldy, void* stream);

@@ -22,6 +22,7 @@ namespace {
 constexpr int kMaxDevices = 64;
 constexpr int kMaxK = 65536;            // 65536 * 128 * 128 = 2^30: the int32 sum cannot overflow
 constexpr int kMaxExperts = 1024;
+constexpr int kMaxSize = 1 << 30;       // rows, channels or columns: their sums with a tile stay below 2^31
 
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 inline elq_status status_of(cudaError_t e) { return e == cudaSuccess ? ELQ_OK : ELQ_ERR_CUDA; }
@@ -422,10 +423,10 @@ elq_status elq_quantize_i8(const void* x, int32_t x_type, int64_t x_rows, int32_
                            void* stream) {
     if (rows < 0 || x_rows < 0 || cols < 1 || ldx < cols || div < 1) return ELQ_ERR_INVALID_ARG;
     if (!index && rows > 0 && (div != 1 || rows > x_rows)) return ELQ_ERR_INVALID_ARG;
-    if (!float_type(x_type)) return ELQ_ERR_UNSUPPORTED;
+    if (!float_type(x_type) || cols > kMaxSize) return ELQ_ERR_UNSUPPORTED;
     const elq_status st = check_codes(q, ldq, scale, rows, cols);
     if (st != ELQ_OK || rows == 0) return st;
-    if (!x && x_rows > 0) return ELQ_ERR_INVALID_ARG;
+    if (!x || x_rows == 0) return ELQ_ERR_INVALID_ARG;
     if (!aligned(x, 16) || !aligned(index, 4)) return ELQ_ERR_ALIGNMENT;
     RowArgs a;
     std::memset(&a, 0, sizeof(a));
@@ -446,8 +447,8 @@ elq_status elq_quantize_i8(const void* x, int32_t x_type, int64_t x_rows, int32_
 
 elq_status elq_swiglu_i8(const void* gu, int32_t x_type, int64_t rows, int32_t I, int64_t ld, int8_t* q, int64_t ldq,
                          float* scale, void* stream) {
-    if (rows < 0 || I < 1 || I > INT32_MAX / 2 || ld < 2ll * I) return ELQ_ERR_INVALID_ARG;
-    if (!float_type(x_type)) return ELQ_ERR_UNSUPPORTED;
+    if (rows < 0 || I < 1 || ld < 2ll * I) return ELQ_ERR_INVALID_ARG;
+    if (!float_type(x_type) || I > kMaxSize) return ELQ_ERR_UNSUPPORTED;
     const elq_status st = check_codes(q, ldq, scale, rows, I);
     if (st != ELQ_OK || rows == 0) return st;
     if (!gu) return ELQ_ERR_INVALID_ARG;
@@ -470,10 +471,10 @@ elq_status elq_combine_i8(const void* o, int32_t o_type, int64_t o_rows, int32_t
                           const float* weights, int64_t T, int32_t k, int8_t* q, int64_t ldq, float* scale,
                           void* stream) {
     if (T < 0 || o_rows < 0 || cols < 1 || ldo < cols || k < 1 || k > 64) return ELQ_ERR_INVALID_ARG;
-    if (!float_type(o_type)) return ELQ_ERR_UNSUPPORTED;
+    if (!float_type(o_type) || cols > kMaxSize) return ELQ_ERR_UNSUPPORTED;
     const elq_status st = check_codes(q, ldq, scale, T, cols);
     if (st != ELQ_OK || T == 0) return st;
-    if ((!o && o_rows > 0) || !pos || !weights) return ELQ_ERR_INVALID_ARG;
+    if (!o || o_rows == 0 || !pos || !weights) return ELQ_ERR_INVALID_ARG;
     if (!aligned(o, 16) || !aligned(pos, 4) || !aligned(weights, 4)) return ELQ_ERR_ALIGNMENT;
     RowArgs a;
     std::memset(&a, 0, sizeof(a));
@@ -496,8 +497,8 @@ elq_status elq_combine_i8(const void* o, int32_t o_type, int64_t o_rows, int32_t
 elq_status elq_i8_matmul(const int8_t* x, int64_t ldx, const float* sx, int64_t T, const int8_t* w, int64_t ldw,
                          const float* sw, const float* bias, int32_t N, int32_t K, void* y, int32_t y_type, int64_t ldy,
                          void* stream) {
-    if (T < 0 || T > INT32_MAX || N < 1 || K < 1 || ldx < K || ldw < K || ldy < N) return ELQ_ERR_INVALID_ARG;
-    if (!float_type(y_type) || K > kMaxK) return ELQ_ERR_UNSUPPORTED;
+    if (T < 0 || N < 1 || K < 1 || ldx < K || ldw < K || ldy < N) return ELQ_ERR_INVALID_ARG;
+    if (!float_type(y_type) || K > kMaxK || T > kMaxSize || N > kMaxSize) return ELQ_ERR_UNSUPPORTED;
     if (ldx % 16 || ldw % 16) return ELQ_ERR_ALIGNMENT;
     if (T == 0) return ELQ_OK;
     if (!x || !sx || !w || !sw || !y) return ELQ_ERR_INVALID_ARG;
@@ -511,11 +512,11 @@ elq_status elq_i8_matmul(const int8_t* x, int64_t ldx, const float* sx, int64_t 
 elq_status elq_grouped_matmul(const void* x, int32_t x_type, int64_t ldx, const float* sx, int64_t M, const void* w,
                               int64_t ldw, int64_t w_stride, const float* sw, int32_t E, int32_t N, int32_t K,
                               const int32_t* offsets, void* y, int32_t y_type, int64_t ldy, void* stream) {
-    if (M < 0 || M > INT32_MAX || E < 1 || N < 1 || K < 1 || ldx < K || ldw < K || ldy < N) return ELQ_ERR_INVALID_ARG;
+    if (M < 0 || E < 1 || N < 1 || K < 1 || ldx < K || ldw < K || ldy < N) return ELQ_ERR_INVALID_ARG;
     if (E > 1 && w_stride < (int64_t)(N - 1) * ldw + K) return ELQ_ERR_INVALID_ARG;
     if (x_type != ELQ_I8 && x_type != ELQ_BF16 && x_type != ELQ_F16) return ELQ_ERR_UNSUPPORTED;
     if (!float_type(y_type) || (x_type != ELQ_I8 && y_type != ELQ_F32 && y_type != x_type)) return ELQ_ERR_UNSUPPORTED;
-    if (K > kMaxK || E > kMaxExperts) return ELQ_ERR_UNSUPPORTED;
+    if (K > kMaxK || E > kMaxExperts || M > kMaxSize || N > kMaxSize) return ELQ_ERR_UNSUPPORTED;
     const int es = type_bytes(x_type);
     if ((ldx * es) % 16 || (ldw * es) % 16 || (E > 1 && (w_stride * es) % 16)) return ELQ_ERR_ALIGNMENT;
     if (M == 0) return ELQ_OK;
@@ -533,7 +534,8 @@ elq_status elq_rms_norm(const void* x, int32_t x_type, int64_t T, int32_t cols, 
                         float eps, void* n, int32_t n_type, int64_t ldn, float* scale, void* stream) {
     if (T < 0 || cols < 1 || ldx < cols || ldn < cols || !(eps > 0.0f) || !std::isfinite(eps))
         return ELQ_ERR_INVALID_ARG;
-    if (!float_type(x_type) || (!float_type(n_type) && n_type != ELQ_I8)) return ELQ_ERR_UNSUPPORTED;
+    if (!float_type(x_type) || (!float_type(n_type) && n_type != ELQ_I8) || cols > kMaxSize)
+        return ELQ_ERR_UNSUPPORTED;
     if (n_type == ELQ_I8) {
         const elq_status st = check_codes((const int8_t*)n, ldn, scale, T, cols);
         if (st != ELQ_OK) return st;
@@ -565,7 +567,7 @@ elq_status elq_residual_norm(const elq_residual* r, void* stream) {
     if (r->T < 0 || r->cols < 1 || r->ldh < r->cols || r->ldy < r->cols || r->ld_out < r->cols)
         return ELQ_ERR_INVALID_ARG;
     if (!(r->eps > 0.0f) || !std::isfinite(r->eps)) return ELQ_ERR_INVALID_ARG;
-    if (!float_type(r->h_type) || !float_type(r->y_type)) return ELQ_ERR_UNSUPPORTED;
+    if (!float_type(r->h_type) || !float_type(r->y_type) || r->cols > kMaxSize) return ELQ_ERR_UNSUPPORTED;
     const bool next = r->n != nullptr;
     if (next) {
         if (!float_type(r->n_type) && r->n_type != ELQ_I8) return ELQ_ERR_UNSUPPORTED;

@@ -158,28 +158,46 @@ __device__ __forceinline__ void gemv_rows(const GemvArgs& a, const uint8_t* w, c
 
 __device__ __forceinline__ int clamp_offset(int o, int M) { return min(max(o, 0), M); }
 
+// Offsets clamped to the rows and raised to the largest before them: groups are
+// then disjoint whatever the array holds.  One batch of 32 (o: this lane's offset),
+// `before` the largest of the batches before, updated.  Warp-collective.
+__device__ __forceinline__ int raise_offsets(int o, int M, int& before) {
+    o = max(clamp_offset(o, M), before);
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, o, d);
+        if (lane >= d) o = max(o, v);
+    }
+    before = __shfl_sync(0xffffffffu, o, 31);
+    return o;
+}
+
 // The want-th (from 0) group that has rows: its expert and rows r0 .. r1-1.
 // Warp-uniform; false if there is none.
 __device__ __forceinline__ bool find_group(const int32_t* offsets, int E, int M, int want, int& e, int& r0, int& r1) {
     const int lane = threadIdx.x & 31;
+    int before = 0;
     for (int e0 = 0; e0 < E; e0 += 128) {
         int lo[4], hi[4];
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
+        for (int b = 0; b < 4; ++b) {       // all loads before the scans
             const int i = e0 + 32 * b + lane;
-            lo[b] = i < E ? clamp_offset(__ldg(offsets + i), M) : 0;
-            hi[b] = i < E ? clamp_offset(__ldg(offsets + i + 1), M) : 0;
+            lo[b] = i < E ? __ldg(offsets + i) : 0;
+            hi[b] = i < E ? __ldg(offsets + i + 1) : 0;
         }
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-            uint32_t m = __ballot_sync(0xffffffffu, hi[b] > lo[b]);
+            const int l0 = raise_offsets(lo[b], M, before);
+            const int h0 = max(l0, clamp_offset(hi[b], M));
+            uint32_t m = __ballot_sync(0xffffffffu, h0 > l0);
             const int c = __popc(m);
             if (want < c) {
                 for (int i = 0; i < want; ++i) m &= m - 1;
                 const int l = __ffs(m) - 1;
                 e = e0 + 32 * b + l;
-                r0 = __shfl_sync(0xffffffffu, lo[b], l);
-                r1 = __shfl_sync(0xffffffffu, hi[b], l);
+                r0 = __shfl_sync(0xffffffffu, l0, l);
+                r1 = __shfl_sync(0xffffffffu, h0, l);
                 return true;
             }
             want -= c;
@@ -190,24 +208,18 @@ __device__ __forceinline__ bool find_group(const int32_t* offsets, int E, int M,
 
 template <int KIND, int R, int U>
 __global__ void __launch_bounds__(32 * kGemvWarps) k_gemv(const __grid_constant__ GemvArgs a) {
-    pdl_trigger();
     pdl_wait();
-    for (int g = blockIdx.y;; g += gridDim.y) {
-        int e = 0, r0 = 0, r1 = a.M;
-        if (a.offsets) {
-            if (!find_group(a.offsets, a.E, a.M, g, e, r0, r1)) return;
-        } else if (g > 0) {
-            return;
-        }
-        const uint8_t* w = a.w + (int64_t)e * a.w_stride;
-        const float* sw = KIND == KIND_I8 ? a.sw + (int64_t)e * a.N : nullptr;
-        for (int n0 = (blockIdx.x * kGemvWarps + (threadIdx.x >> 5)) * R; n0 < a.N; n0 += gridDim.x * kGemvWarps * R) {
-            for (int t0 = r0; t0 < r1; t0 += 4) {
-                const int nt = min(4, r1 - t0);
-                if (nt == 1) gemv_rows<KIND, R, 1, U>(a, w, sw, n0, t0, nt);
-                else if (nt == 2) gemv_rows<KIND, R, 2, U>(a, w, sw, n0, t0, nt);
-                else gemv_rows<KIND, R, 4, U>(a, w, sw, n0, t0, nt);
-            }
+    pdl_trigger();
+    int e = 0, r0 = 0, r1 = a.M;        // at most min(E, M) groups have rows, and the grid has that many
+    if (a.offsets && !find_group(a.offsets, a.E, a.M, blockIdx.y, e, r0, r1)) return;
+    const uint8_t* w = a.w + (int64_t)e * a.w_stride;
+    const float* sw = KIND == KIND_I8 ? a.sw + (int64_t)e * a.N : nullptr;
+    for (int n0 = (blockIdx.x * kGemvWarps + (threadIdx.x >> 5)) * R; n0 < a.N; n0 += gridDim.x * kGemvWarps * R) {
+        for (int t0 = r0; t0 < r1; t0 += 4) {
+            const int nt = min(4, r1 - t0);
+            if (nt == 1) gemv_rows<KIND, R, 1, U>(a, w, sw, n0, t0, nt);
+            else if (nt == 2) gemv_rows<KIND, R, 2, U>(a, w, sw, n0, t0, nt);
+            else gemv_rows<KIND, R, 4, U>(a, w, sw, n0, t0, nt);
         }
     }
 }

@@ -249,7 +249,7 @@ struct Unit {
     int e, ch0, row0, rows, n;      // expert, first channel, first row, rows, the MMA's N
 };
 
-// s_off: the clamped offsets; s_tile[e]: row tiles of the experts before e; tiles
+// s_off: the offsets, clamped and raised; s_tile[e]: row tiles of the experts before e; tiles
 // have rows in steps of 16 (32 in a pair, where each CTA brings half of them).
 template <int CG>
 __device__ __forceinline__ Unit unit_of(int u, const int* s_off, const int* s_tile, int E, int ch_tiles) {
@@ -357,23 +357,28 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_mma(const __grid_constant__ 
     }
     if (warp == 2) tmem_alloc<CG>(s_tmem, 512);
     if (warp == 3 && lane < 2) prefetch_map(lane ? &a.tx : &a.tw);
-    pdl_trigger();
     pdl_wait();
-    for (int i = threadIdx.x; i <= a.E; i += kMmaThreads)
-        s_off[i] = a.offsets ? clamp_offset(__ldg(a.offsets + i), a.M) : (i ? a.M : 0);
+    pdl_trigger();
+    for (int i = threadIdx.x; i <= a.E; i += kMmaThreads) s_off[i] = a.offsets ? __ldg(a.offsets + i) : (i ? a.M : 0);
     __syncthreads();
     if (warp == 0) {
-        int before = 0;
+        int top = 0, before = 0;        // the largest offset so far; row tiles so far
         for (int e0 = 0; e0 < a.E; e0 += 32) {
             const int e = e0 + lane;
-            const int c = e < a.E ? max(0, s_off[e + 1] - s_off[e]) : 0;
-            int t = (c + a.bn - 1) / a.bn, s = t;
+            const int raw = e < a.E ? s_off[e + 1] : 0;         // this batch reads it before the next writes over it
+            const int lo = raise_offsets(e < a.E ? s_off[e] : 0, a.M, top);
+            const int hi = e < a.E ? max(lo, clamp_offset(raw, a.M)) : lo;
+            int t = (hi - lo + a.bn - 1) / a.bn, s = t;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int v = __shfl_up_sync(0xffffffffu, s, o);
                 if (lane >= o) s += v;
             }
-            if (e < a.E) s_tile[e] = before + s - t;
+            if (e < a.E) {
+                s_off[e] = lo;
+                s_tile[e] = before + s - t;
+                if (e == a.E - 1) s_off[a.E] = hi;
+            }
             before += __shfl_sync(0xffffffffu, s, 31);
         }
         if (lane == 0) s_tile[a.E] = before;
@@ -551,8 +556,8 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_split(const __grid_constant_
     }
     if (warp == 2) tmem_alloc<1>(s_tmem, 256);
     if (warp == 3 && lane < 2) prefetch_map(lane ? &a.tx : &a.tw);
-    pdl_trigger();
     pdl_wait();
+    pdl_trigger();
     __syncwarp();
     tc_before();
     __syncthreads();

@@ -525,9 +525,9 @@ __device__ __forceinline__ void norm8(const float* wt, int i, int cols, float rs
 template <int OP, int VPT, bool VEC>
 __global__ void __launch_bounds__(kRowThreads) k_rows(const __grid_constant__ RowArgs a) {
     __shared__ __align__(16) uint32_t red[2][16];
-    pdl_trigger();
     RowReduce<false> rr(red);
     pdl_wait();
+    pdl_trigger();
     const int nch = (int)((a.cols + 8ll * blockDim.x - 1) / (8ll * blockDim.x));      // chunks of a thread
     constexpr int NV = VPT > 0 ? VPT : 1;
     const bool codes = a.n_type == ELQ_I8;
@@ -793,8 +793,8 @@ __global__ void __launch_bounds__(VPT == 1 ? kRowThreads : kPipeThreads4, 2) k_p
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 
-    pdl_trigger();
     pdl_wait();
+    pdl_trigger();
     int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     const int64_t step = (int64_t)gridDim.x * blockDim.y;
     const float* w_last = OP == ROW_RMS ? a.w : a.n ? a.w_next : nullptr;     // of the norm that is written

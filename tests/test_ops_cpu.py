@@ -43,8 +43,8 @@ QUANT = dict(x=P, x_type=0, x_rows=4, cols=64, ldx=64, index=None, div=1, rows=4
 @pytest.mark.parametrize("over,status", [
     (dict(rows=-1), -1), (dict(x_rows=-1), -1), (dict(cols=0), -1), (dict(ldx=63), -1), (dict(div=0), -1),
     (dict(rows=5), -1), (dict(div=2), -1), (dict(x_type=24), -2), (dict(x_type=2), -2), (dict(ldq=48), -1),
-    (dict(ldq=72), -3), (dict(q=None), -1), (dict(scale=None), -1), (dict(x=None), -1), (dict(x=P + 8), -3),
-    (dict(q=P + 8), -3), (dict(scale=P + 2), -3), (dict(index=P + 2), -3),
+    (dict(ldq=72), -3), (dict(q=None), -1), (dict(scale=None), -1), (dict(x=None), -1), (dict(x_rows=0, index=P), -1), (dict(cols=(1 << 30) + 1, ldx=1 << 31, ldq=1 << 31), -2),
+    (dict(x=P + 8), -3), (dict(q=P + 8), -3), (dict(scale=P + 2), -3), (dict(index=P + 2), -3),
     (dict(rows=0), 0), (dict(rows=0, x=None, q=None, scale=None, x_rows=0), 0)])
 def test_quantize_refusals(L, over, status):
     assert L.elq_quantize_i8(*_args(QUANT, over)) == status
@@ -65,7 +65,7 @@ COMBINE = dict(o=P, o_type=0, o_rows=8, cols=64, ldo=64, pos=P, weights=P, T=4, 
 
 @pytest.mark.parametrize("over,status", [
     (dict(T=-1), -1), (dict(o_rows=-1), -1), (dict(k=0), -1), (dict(k=65), -1), (dict(ldo=60), -1), (dict(o_type=24), -2),
-    (dict(pos=None), -1), (dict(weights=None), -1), (dict(o=None), -1), (dict(o=P + 4), -3), (dict(pos=P + 1), -3),
+    (dict(pos=None), -1), (dict(weights=None), -1), (dict(o_rows=0), -1), (dict(o=None), -1), (dict(o=P + 4), -3), (dict(pos=P + 1), -3),
     (dict(ldq=65), -3), (dict(T=0, pos=None, weights=None), 0)])
 def test_combine_refusals(L, over, status):
     assert L.elq_combine_i8(*_args(COMBINE, over)) == status
@@ -75,7 +75,7 @@ MATMUL = dict(x=P, ldx=64, sx=P, T=4, w=P, ldw=64, sw=P, bias=None, N=32, K=64, 
 
 
 @pytest.mark.parametrize("over,status", [
-    (dict(T=-1), -1), (dict(T=1 << 31), -1), (dict(N=0), -1), (dict(K=0), -1), (dict(ldx=48), -1), (dict(ldw=48), -1),
+    (dict(T=-1), -1), (dict(T=(1 << 30) + 1), -2), (dict(N=(1 << 30) + 1, ldy=1 << 31), -2), (dict(N=0), -1), (dict(K=0), -1), (dict(ldx=48), -1), (dict(ldw=48), -1),
     (dict(ldy=31), -1), (dict(y_type=24), -2), (dict(K=65537, ldx=65552, ldw=65552), -2), (dict(ldx=72), -3),
     (dict(ldw=72), -3), (dict(x=None), -1), (dict(sx=None), -1), (dict(w=None), -1), (dict(sw=None), -1),
     (dict(y=None), -1), (dict(x=P + 8), -3), (dict(w=P + 8), -3), (dict(y=P + 8), -3), (dict(bias=P + 2), -3),
@@ -90,7 +90,7 @@ G16 = dict(x_type=30, sx=None, sw=None)
 
 
 @pytest.mark.parametrize("over,status", [
-    (dict(M=-1), -1), (dict(M=1 << 31), -1), (dict(E=0), -1), (dict(E=1025), -2), (dict(N=0), -1), (dict(K=0), -1),
+    (dict(M=-1), -1), (dict(M=(1 << 30) + 1), -2), (dict(N=(1 << 30) + 1, ldy=1 << 31, w_stride=1 << 40), -2), (dict(E=0), -1), (dict(E=1025), -2), (dict(N=0), -1), (dict(K=0), -1),
     (dict(w_stride=64 * 32 - 16), -1), (dict(w_stride=64 * 32 + 8), -3), (dict(ldx=72), -3), (dict(ldy=31), -1),
     (dict(x_type=0), -2), (dict(y_type=24), -2), (dict(offsets=None), -1), (dict(sx=None), -1), (dict(sw=None), -1),
     (dict(x_type=30), -1), (dict(G16, y_type=1), -2), (dict(G16, ldx=68), -3), (dict(G16, K=65537, ldx=65544, ldw=65544, w_stride=65544 * 32), -2),
@@ -103,7 +103,7 @@ RMS = dict(x=P, x_type=0, T=4, cols=64, ldx=64, weight=None, eps=1e-6, n=2 * P, 
 
 
 @pytest.mark.parametrize("over,status", [
-    (dict(T=-1), -1), (dict(cols=0), -1), (dict(ldx=60), -1), (dict(ldn=60), -1), (dict(eps=0.0), -1),
+    (dict(T=-1), -1), (dict(cols=0), -1), (dict(cols=(1 << 30) + 1, ldx=1 << 31, ldn=1 << 31), -2), (dict(ldx=60), -1), (dict(ldn=60), -1), (dict(eps=0.0), -1),
     (dict(eps=float("nan")), -1), (dict(eps=float("inf")), -1), (dict(x_type=24), -2), (dict(n_type=9), -2),
     (dict(scale=P), -1), (dict(n_type=24), -1), (dict(n_type=24, scale=P, ldn=72), -3), (dict(x=None), -1),
     (dict(n=None), -1), (dict(n=P, n_type=30), -1), (dict(n=P, ldn=68), -1), (dict(x=P + 4), -3),
