@@ -401,11 +401,11 @@ elq_status launch_mma(const Product& p, cudaStream_t s) {
 
 // The register GEMV for grouped products of up to 8 rows (above, the tensor cores
 // read the weights faster: 16 rows of 16 experts); dense ones of up to 4, or 8 of a
-// matrix below 1 MB (6 rows 4096 -> 1792: 6.2 us against 5.5 split over K; 512 ->
-// 512: 1.9 against 4.2).
+// matrix below 256 KB (4096 -> 1792: 4.3 us for one row, 6.1 for four, 8.9 for six,
+// against 5.2 split over K; 512 -> 512, six rows: 1.9 against 3.1).
 bool few_rows(const Product& p) {
     if (p.offsets || p.M <= 4) return p.M <= 8;
-    return p.M <= 8 && (int64_t)p.N * p.K * (p.kind == KIND_I8 ? 1 : 2) <= 1 << 20;
+    return p.M <= 8 && (int64_t)p.N * p.K * (p.kind == KIND_I8 ? 1 : 2) <= 1 << 18;
 }
 
 elq_status run_product(const Product& p, cudaStream_t s) {
