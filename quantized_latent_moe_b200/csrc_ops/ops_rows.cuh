@@ -313,30 +313,57 @@ __device__ __forceinline__ int elem(int i, int j) {
     return VEC ? 8 * (i * (int)blockDim.x + (int)threadIdx.x) + j : (8 * i + j) * (int)blockDim.x + (int)threadIdx.x;
 }
 
+// Eight values of a row as they are stored (a whole VEC chunk of 16-bit values in
+// the first four words), and those as fp32.  Apart, so that the loads of several
+// rows can be in flight before the first is converted.
+struct Raw8 {
+    uint32_t r[8];
+};
+
 template <bool VEC>
-__device__ __forceinline__ void get8(const void* p, int type, int64_t row0, int i, int cols, float (&v)[8]) {
+__device__ __forceinline__ void load_raw(const void* p, int type, int64_t row0, int i, int cols, Raw8& raw) {
     if (VEC && elem<VEC>(i, 0) + 8 <= cols) {
-        load8(p, type, row0 + elem<VEC>(i, 0), v);
-        return;
-    }
-    // all eight loads before any conversion, so that they are in flight together
-    if (type == ELQ_F32) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int e = elem<VEC>(i, j);
-            v[j] = e < cols ? reinterpret_cast<const float*>(p)[row0 + e] : 0.0f;
+        const char* q = reinterpret_cast<const char*>(p) + (row0 + elem<VEC>(i, 0)) * (type == ELQ_F32 ? 4 : 2);
+        const uint4 a = reinterpret_cast<const uint4*>(q)[0];
+        raw.r[0] = a.x; raw.r[1] = a.y; raw.r[2] = a.z; raw.r[3] = a.w;
+        if (type == ELQ_F32) {
+            const uint4 b = reinterpret_cast<const uint4*>(q)[1];
+            raw.r[4] = b.x; raw.r[5] = b.y; raw.r[6] = b.z; raw.r[7] = b.w;
         }
         return;
     }
-    uint32_t r[8];
+    if (type == ELQ_F32) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const int e = elem<VEC>(i, j);
-        r[j] = e < cols ? reinterpret_cast<const uint16_t*>(p)[row0 + e] : 0;
+        for (int j = 0; j < 8; ++j)
+            raw.r[j] = elem<VEC>(i, j) < cols ? reinterpret_cast<const uint32_t*>(p)[row0 + elem<VEC>(i, j)] : 0;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            raw.r[j] = elem<VEC>(i, j) < cols ? reinterpret_cast<const uint16_t*>(p)[row0 + elem<VEC>(i, j)] : 0;
     }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void raw_values(const Raw8& raw, int type, int i, int cols, float (&v)[8]) {
+    if (type == ELQ_F32) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        v[j] = type == ELQ_BF16 ? bf16_lo(r[j]) : __half2float(__ushort_as_half((unsigned short)r[j]));
+        for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(raw.r[j]);
+    } else if (VEC && elem<VEC>(i, 0) + 8 <= cols) {
+        widen8(make_uint4(raw.r[0], raw.r[1], raw.r[2], raw.r[3]), type, v);
+    } else if (type == ELQ_BF16) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = bf16_lo(raw.r[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = __half2float(__ushort_as_half((unsigned short)raw.r[j]));
+    }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void get8(const void* p, int type, int64_t row0, int i, int cols, float (&v)[8]) {
+    Raw8 raw;
+    load_raw<VEC>(p, type, row0, i, cols, raw);
+    raw_values<VEC>(raw, type, i, cols, v);
 }
 
 template <bool VEC>
@@ -424,8 +451,8 @@ __device__ __forceinline__ f32x2 swiglu2(f32x2 g, f32x2 u) {
 }
 
 // The eight source values of chunk ci of output row `row` (the quantisers'
-// inputs before quantising, or the x of a norm).
-template <int OP, bool VEC>
+// inputs before quantising, or the x of a norm).  B: rows of a combine in flight.
+template <int OP, bool VEC, int B>
 __device__ __forceinline__ void source8(const RowArgs& a, int64_t row, int64_t src, int ci, float (&v)[8]) {
     if (OP == ROW_QUANT) {
         if (src < 0) {
@@ -436,8 +463,11 @@ __device__ __forceinline__ void source8(const RowArgs& a, int64_t row, int64_t s
         }
     } else if (OP == ROW_SWIGLU) {
         float u[8];
-        get8<VEC>(a.x, a.x_type, row * a.ldx, ci, a.cols, v);
-        get8<VEC>(a.x, a.x_type, row * a.ldx + a.cols, ci, a.cols, u);
+        Raw8 rg, ru;
+        load_raw<VEC>(a.x, a.x_type, row * a.ldx, ci, a.cols, rg);
+        load_raw<VEC>(a.x, a.x_type, row * a.ldx + a.cols, ci, a.cols, ru);
+        raw_values<VEC>(rg, a.x_type, ci, a.cols, v);
+        raw_values<VEC>(ru, a.x_type, ci, a.cols, u);
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
             const float2 h = halves(swiglu2(pair(v[j], v[j + 1]), pair(u[j], u[j + 1])));
@@ -447,24 +477,27 @@ __device__ __forceinline__ void source8(const RowArgs& a, int64_t row, int64_t s
     } else if (OP == ROW_COMBINE) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-        for (int i0 = 0; i0 < a.k; i0 += 4) {
-            float w[4], o[4][8];
+        // B rows at a time: all their positions, then all their pieces, in flight together
+        for (int i0 = 0; i0 < a.k; i0 += B) {
+            float w[B];
+            int64_t p[B];
+            Raw8 raw[B];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int64_t p = i0 + i < a.k ? a.index[row * a.k + i0 + i] : -1;
-                const bool on = p >= 0 && p < a.x_rows;
-                w[i] = on ? a.weights[row * a.k + i0 + i] : 0.0f;
-                if (on) {
-                    get8<VEC>(a.x, a.x_type, p * a.ldx, ci, a.cols, o[i]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) o[i][j] = 0.0f;
-                }
+            for (int i = 0; i < B; ++i) {
+                p[i] = i0 + i < a.k ? a.index[row * a.k + i0 + i] : -1;
+                w[i] = i0 + i < a.k ? a.weights[row * a.k + i0 + i] : 0.0f;
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < B; ++i)
+                if (p[i] >= 0 && p[i] < a.x_rows) load_raw<VEC>(a.x, a.x_type, p[i] * a.ldx, ci, a.cols, raw[i]);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = __fmaf_rn(w[i], o[i][j], v[j]);
+            for (int i = 0; i < B; ++i) {
+                if (p[i] < 0 || p[i] >= a.x_rows) continue;
+                float o[8];
+                raw_values<VEC>(raw[i], a.x_type, ci, a.cols, o);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = __fmaf_rn(w[i], o[j], v[j]);
+            }
         }
     } else {
         get8<VEC>(a.x, a.x_type, row * a.ldx, ci, a.cols, v);
@@ -485,25 +518,23 @@ __device__ __forceinline__ float residual1(float y, float rstd, float w, float g
     return __fmaf_rn(g, __fmul_rn(__fmul_rn(y, rstd), w), __fmul_rn(res_scale, h));
 }
 
+// The gate's values of chunk i.
+template <bool VEC>
+__device__ __forceinline__ void gate8(const RowArgs& a, int64_t row, int i, float (&g)[8]) {
+    const float* gr = a.gate ? a.gate + (row / a.gate_rows) * a.gate_ld : nullptr;
+    if (gr && a.gate_cols == 1) {
+        const float g0 = gr[0];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) g[j] = g0;
+    } else {
+        weight8<VEC>(gr, i, a.cols, g);
+    }
+}
+
 // v (y's values) -> h' = res_scale * h + gate * (y * rstd * w); 0 past the end.
 template <bool VEC>
-__device__ __forceinline__ void residual8(const RowArgs& a, int64_t row, int i, float rstd, const float (&h)[8],
-                                          float (&v)[8]) {
-    float w[8], g[8];
-    weight8<VEC>(a.w, i, a.cols, w);
-    if (!a.gate) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) g[j] = 1.0f;
-    } else {
-        const float* gr = a.gate + (row / a.gate_rows) * a.gate_ld;
-        if (a.gate_cols == 1) {
-            const float g0 = gr[0];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) g[j] = g0;
-        } else {
-            get8<VEC>(gr, ELQ_F32, 0, i, a.cols, g);
-        }
-    }
+__device__ __forceinline__ void residual8(const RowArgs& a, int i, float rstd, const float (&w)[8], const float (&g)[8],
+                                          const float (&h)[8], float (&v)[8]) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const float r = residual1(v[j], rstd, w[j], g[j], a.res_scale, h[j]);
@@ -512,10 +543,7 @@ __device__ __forceinline__ void residual8(const RowArgs& a, int64_t row, int i, 
 }
 
 // v -> v * rstd * w, the normalised row.
-template <bool VEC>
-__device__ __forceinline__ void norm8(const float* wt, int i, int cols, float rstd, float (&v)[8]) {
-    float w[8];
-    weight8<VEC>(wt, i, cols, w);
+__device__ __forceinline__ void norm8(const float (&w)[8], float rstd, float (&v)[8]) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(__fmul_rn(v[j], rstd), w[j]);
 }
@@ -523,13 +551,13 @@ __device__ __forceinline__ void norm8(const float* wt, int i, int cols, float rs
 // VPT: chunks a thread holds in registers (VPT * blockDim.x >= ceil(cols / 8)),
 // or 0: none, every step reads its inputs again.
 template <int OP, int VPT, bool VEC>
-__global__ void __launch_bounds__(kRowThreads) k_rows(const __grid_constant__ RowArgs a) {
+__global__ void __launch_bounds__(kRowThreads, VPT == 1 && OP != ROW_COMBINE ? 2 : 1) k_rows(const __grid_constant__ RowArgs a) {
     __shared__ __align__(16) uint32_t red[2][16];
     RowReduce<false> rr(red);
     pdl_wait();
     pdl_trigger();
     const int nch = (int)((a.cols + 8ll * blockDim.x - 1) / (8ll * blockDim.x));      // chunks of a thread
-    constexpr int NV = VPT > 0 ? VPT : 1;
+    constexpr int NV = VPT > 0 ? VPT : 1, B = VPT == 1 ? 8 : VPT == 2 ? 4 : 2;
     const bool codes = a.n_type == ELQ_I8;
     int8_t* q = reinterpret_cast<int8_t*>(a.n);
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
@@ -540,16 +568,31 @@ __global__ void __launch_bounds__(kRowThreads) k_rows(const __grid_constant__ Ro
         }
         float v[NV][8];
         if constexpr (VPT > 0) {
-            float h[OP == ROW_RESIDUAL ? NV : 1][8];
+            constexpr bool NORM = OP == ROW_RMS || OP == ROW_RESIDUAL;
+            const float* w_last = OP == ROW_RMS ? a.w : a.w_next;
+            // One chunk a thread: the weights too are fetched before the first reduction.
+            constexpr bool EARLY = VPT == 1;
+            float h[OP == ROW_RESIDUAL ? NV : 1][8], w[8], g[8], wn[8];
+            if constexpr (EARLY && OP == ROW_RESIDUAL) {
+                weight8<VEC>(a.w, 0, a.cols, w);
+                gate8<VEC>(a, row, 0, g);
+            }
+            if constexpr (EARLY && NORM) weight8<VEC>(w_last, 0, a.cols, wn);
+            if constexpr (OP == ROW_RESIDUAL) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
+                for (int i = 0; i < NV; ++i) {      // past the last chunk these are zeros
+                    Raw8 ry, rh;
+                    load_raw<VEC>(a.x, a.x_type, row * a.ldx, i, a.cols, ry);
+                    load_raw<VEC>(a.h, a.h_type, row * a.ldh, i, a.cols, rh);
+                    raw_values<VEC>(ry, a.x_type, i, a.cols, v[i]);
+                    raw_values<VEC>(rh, a.h_type, i, a.cols, h[i]);
+                }
+            } else {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
-                if (i < nch) source8<OP, VEC>(a, row, src, i, v[i]);
-                if constexpr (OP == ROW_RESIDUAL) {
+                for (int i = 0; i < NV; ++i) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) h[i][j] = 0.0f;
-                    if (i < nch) get8<VEC>(a.h, a.h_type, row * a.ldh, i, a.cols, h[i]);
+                    for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
+                    if (i < nch) source8<OP, VEC, B>(a, row, src, i, v[i]);
                 }
             }
             if constexpr (OP == ROW_RESIDUAL) {
@@ -559,22 +602,26 @@ __global__ void __launch_bounds__(kRowThreads) k_rows(const __grid_constant__ Ro
                 const float rstd = rstd_of(rr.sum(ss), a.inv_cols, a.eps);
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
-                        if (i >= nch) continue;
-                    residual8<VEC>(a, row, i, rstd, h[i], v[i]);
+                    if (i >= nch) continue;
+                    if constexpr (!EARLY) {
+                        weight8<VEC>(a.w, i, a.cols, w);
+                        gate8<VEC>(a, row, i, g);
+                    }
+                    residual8<VEC>(a, i, rstd, w, g, h[i], v[i]);
                     put8<VEC>(a.h_out, a.h_type, row * a.ld_out, i, a.cols, v[i]);
                 }
                 if (!a.n) continue;
             }
-            if constexpr (OP == ROW_RMS || OP == ROW_RESIDUAL) {
+            if constexpr (NORM) {
                 float ss = 0.0f;
 #pragma unroll
                 for (int i = 0; i < NV; ++i) ss = sumsq8(ss, v[i]);
                 const float rstd = rstd_of(rr.sum(ss), a.inv_cols, a.eps);
-                const float* wt = OP == ROW_RMS ? a.w : a.w_next;
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
-                        if (i >= nch) continue;
-                    norm8<VEC>(wt, i, a.cols, rstd, v[i]);
+                    if (i >= nch) continue;
+                    if constexpr (!EARLY) weight8<VEC>(w_last, i, a.cols, wn);
+                    norm8(wn, rstd, v[i]);
                     if (!codes) put8<VEC>(a.n, a.n_type, row * a.ldn, i, a.cols, v[i]);
                 }
                 if (!codes) continue;
@@ -594,18 +641,24 @@ __global__ void __launch_bounds__(kRowThreads) k_rows(const __grid_constant__ Ro
             // the row's values at chunk i: source, then the residual update,
             // as far as the statistics so far allow
             auto value = [&](int i) {
-                source8<OP, VEC>(a, row, src, i, t);
+                source8<OP, VEC, B>(a, row, src, i, t);
                 if constexpr (OP == ROW_RESIDUAL) {
-                    float h[8];
+                    float h[8], w[8], g[8];
                     get8<VEC>(a.h, a.h_type, row * a.ldh, i, a.cols, h);
-                    residual8<VEC>(a, row, i, rstd, h, t);
+                    weight8<VEC>(a.w, i, a.cols, w);
+                    gate8<VEC>(a, row, i, g);
+                    residual8<VEC>(a, i, rstd, w, g, h, t);
                 }
             };
-            const float* wt = OP == ROW_RMS ? a.w : a.w_next;
+            auto normed = [&](int i) {
+                float w[8];
+                weight8<VEC>(OP == ROW_RMS ? a.w : a.w_next, i, a.cols, w);
+                norm8(w, rstd2, t);
+            };
             if constexpr (OP == ROW_RESIDUAL) {
                 float ss = 0.0f;
                 for (int i = 0; i < nch; ++i) {
-                    source8<OP, VEC>(a, row, src, i, t);
+                    source8<OP, VEC, B>(a, row, src, i, t);
                     ss = sumsq8(ss, t);
                 }
                 rstd = rstd_of(rr.sum(ss), a.inv_cols, a.eps);
@@ -623,7 +676,7 @@ __global__ void __launch_bounds__(kRowThreads) k_rows(const __grid_constant__ Ro
                 float m = 0.0f;
                 for (int i = 0; i < nch; ++i) {
                     value(i);
-                    if (OP == ROW_RMS || OP == ROW_RESIDUAL) norm8<VEC>(wt, i, a.cols, rstd2, t);
+                    if (OP == ROW_RMS || OP == ROW_RESIDUAL) normed(i);
                     m = amax8(m, t);
                 }
                 cs = code_scale(rr.max(__float_as_uint(m)));
@@ -634,7 +687,7 @@ __global__ void __launch_bounds__(kRowThreads) k_rows(const __grid_constant__ Ro
             for (int i = 0; i < nch; ++i) {
                 value(i);
                 if (OP == ROW_RESIDUAL) put8<VEC>(a.h_out, a.h_type, row * a.ld_out, i, a.cols, t);
-                if (OP == ROW_RMS || (OP == ROW_RESIDUAL && a.n)) norm8<VEC>(wt, i, a.cols, rstd2, t);
+                if (OP == ROW_RMS || (OP == ROW_RESIDUAL && a.n)) normed(i);
                 if (!a.n) continue;
                 if (codes) put_codes8<VEC>(q, row * a.ldn, i, a.cols, t, cs);
                 else put8<VEC>(a.n, a.n_type, row * a.ldn, i, a.cols, t);
