@@ -145,16 +145,19 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
+// Not the .aligned forms: those take a warp to be converged, and lanes that waited
+// for an elected one's long loop need not be.
 __device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
-// The cluster address of the pair's first CTA's copy of a shared-memory object.
-__device__ __forceinline__ uint32_t first_cta(const void* p) {
+// The cluster address of a CTA's copy of a shared-memory object.
+__device__ __forceinline__ uint32_t in_cta(const void* p, int rank) {
     uint32_t r;
-    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_addr(p)));
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_addr(p)), "r"(rank));
     return r;
 }
+__device__ __forceinline__ uint32_t first_cta(const void* p) { return in_cta(p, 0); }
 __device__ __forceinline__ void bar_arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -241,6 +244,32 @@ __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatil
     *abort_v = 1;
     atomicExch(&g_ops_err, 1);
     return false;
+}
+
+// The end of a cluster's work: no CTA leaves, and gives up its shared memory, while
+// another may still reach it.  Every CTA tells all `n` of them, itself included
+// (`bye` counts n), and waits, with a limit, for all to have told it.  By all threads.
+__device__ __forceinline__ void cluster_leave(uint64_t* bye, int n) {
+    __syncthreads();
+    if ((int)threadIdx.x < n) bar_arrive_cluster(in_cta(bye, threadIdx.x));
+    if (threadIdx.x == 0) {
+        const uint64_t t0 = global_timer_ns();
+        uint32_t ok = 0;
+        while (!ok) {
+            asm volatile(
+                "{\n\t.reg .pred p;\n\t"
+                "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], 0;\n\t"
+                "selp.u32 %0, 1, 0, p;\n\t}"
+                : "=r"(ok)
+                : "r"(smem_addr(bye))
+                : "memory");
+            if (!ok && global_timer_ns() - t0 > kOpsWaitNs + 10 * kOpsDrainNs) {
+                atomicExch(&g_ops_err, 2);
+                break;
+            }
+        }
+    }
+    __syncthreads();
 }
 
 // ---- units -----------------------------------------------------------------------
@@ -334,7 +363,8 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_mma(const __grid_constant__ 
     uint64_t* tfull = empty + kMmaStagesMax;
     uint64_t* tempty = tfull + 2;
     uint64_t* drain = tempty + 2;
-    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drain + 1);
+    uint64_t* bye = drain + 1;
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bye + 1);
     volatile int* abort_v = reinterpret_cast<volatile int*>(s_tmem + 1);
     float* s_sx = reinterpret_cast<float*>(smem + 512);
     int* s_off = reinterpret_cast<int*>(smem + kMmaHdr);
@@ -352,6 +382,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_mma(const __grid_constant__ 
             mbar_init(tempty + i, kMmaEpiWarps * CG);
         }
         mbar_init(drain, 1);
+        mbar_init(bye, CG);
         *abort_v = 0;
         fence_barrier_init();
     }
@@ -485,6 +516,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_mma(const __grid_constant__ 
             tc_after();
             for (int c = half * 32; c < x.rows; c += 64) {
                 uint32_t r[32];
+                __syncwarp();
                 tmem_read32(tmem + acc * 256 + c + ((uint32_t)(q * 32) << 16), r);
                 const int nr = min(32, x.rows - c);
                 if (KIND == KIND_I8) {
@@ -513,7 +545,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_mma(const __grid_constant__ 
     __syncwarp();
     tc_before();
     if (CG == 1) __syncthreads();
-    else cluster_sync();        // neither CTA leaves while the other may still reach its memory
+    else cluster_leave(bye, CG);
     tc_after();
     if (warp == 2) tmem_free<CG>(tmem, 512);
 }
@@ -533,7 +565,8 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_split(const __grid_constant_
     uint64_t* full = reinterpret_cast<uint64_t*>(smem);
     uint64_t* empty = full + kMmaStagesMax;
     uint64_t* tfull = empty + kMmaStagesMax;
-    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(tfull + 1);
+    uint64_t* bye = tfull + 1;
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bye + 1);
     volatile int* abort_v = reinterpret_cast<volatile int*>(s_tmem + 1);
     const uint32_t tiles0 = (smem_addr(smem) + 512 + 1023u) & ~1023u;
     const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
@@ -551,10 +584,15 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_split(const __grid_constant_
             mbar_init(empty + i, 1);
         }
         mbar_init(tfull, 1);
+        mbar_init(bye, S);
         *abort_v = 0;
         fence_barrier_init();
     }
-    if (warp == 2) tmem_alloc<1>(s_tmem, 256);
+    // as many TMEM columns as the tile has: the CTAs that fit an SM by shared memory
+    // must all get theirs, or clusters that share SMs could wait for one another
+    uint32_t cols = 32;
+    while ((int)cols < a.bn) cols *= 2;
+    if (warp == 2) tmem_alloc<1>(s_tmem, cols);
     if (warp == 3 && lane < 2) prefetch_map(lane ? &a.tx : &a.tw);
     pdl_wait();
     pdl_trigger();
@@ -635,9 +673,9 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_split(const __grid_constant_
     }
     __syncwarp();
     tc_before();
-    cluster_sync();
+    cluster_sync();         // all partials are there
     tc_after();
-    if (warp == 2) tmem_free<1>(tmem, 256);
+    if (warp == 2) tmem_free<1>(tmem, cols);
     // this CTA's rows: a warp one row, a lane four channels
     const int r0 = rows * rank / S, r1 = rows * (rank + 1) / S, ch = ch0 + 4 * lane;
     float sw[4] = {1.0f, 1.0f, 1.0f, 1.0f}, bias[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -709,8 +747,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_split(const __grid_constant_
                 if (ch + j < a.N) store1(a.y, a.y_type, at + j, v[j]);
         }
     }
-    __syncwarp();
-    cluster_sync();         // no CTA leaves while another may still read its partials
+    cluster_leave(bye, S);
 }
 
 }  // namespace elqops
