@@ -24,7 +24,9 @@
  *    is rounded once, to nearest even, to its type.
  *  - Rows, channels and columns number at most 2^30 each.
  *  - No workspace, no allocation, nothing kept between calls but what elq.h
- *    names; any stream, capturable; calls do not share anything on the GPU.
+ *    names; any stream, capturable; calls share nothing on the GPU but the error
+ *    word below.  A call's kernel may be launched while the kernel before it on
+ *    the stream drains; it touches no memory before that one is complete.
  *    An output may not overlap an input, except where in-place use is said.
  *  - Every sum runs in a fixed order: the same call gives the same bits.
  *  - Device data out of range (row indices, positions, group offsets) never
@@ -67,8 +69,8 @@ elq_status elq_quantize_i8(const void* x, int32_t x_type, int64_t x_rows, int32_
                            float* scale, void* stream);
 
 /* SwiGLU, then the row quantiser: row i of gu is I gate values, then I up
- * values (ld >= 2 I); h = (g / (1 + exp(-g))) * u in fp32 (exp within 2^-21 of
- * its value), quantised to q [rows][I] and scale [rows]. */
+ * values (ld >= 2 I); h = (g / (1 + exp(-g))) * u in fp32, within 2^-21 of its
+ * value (or 2^-118 |u|, where g < -87), quantised to q [rows][I] and scale [rows]. */
 elq_status elq_swiglu_i8(const void* gu, int32_t x_type, int64_t rows, int32_t I, int64_t ld, int8_t* q,
                          int64_t ldq, float* scale, void* stream);
 
@@ -123,7 +125,8 @@ elq_status elq_rms_norm(const void* x, int32_t x_type, int64_t T, int32_t cols, 
  *   v  = y[t] / sqrt(mean(y[t]^2) + eps) * post_weight
  *   h' = res_scale * h[t] + gate * v
  *   n  = h' / sqrt(mean(h'^2) + eps) * next_weight        (of the unrounded h')
- * All of it fp32, h' and n each rounded once. */
+ * All of it fp32 (where all rows share the gate it meets post_weight first), h'
+ * and n each rounded once. */
 typedef struct {
     int64_t T;
     int32_t cols;

@@ -15,6 +15,12 @@
 // (channels) it may, 32 rows at a time, rescales, and writes.  Rows of a copied
 // box that belong to the next group, or lie past the matrix (zeros), only meet
 // accumulator columns that are not written.
+//
+// These kernels overlap with no other: they are launched plainly, and let the
+// kernel after them start no earlier than their end.  A chain of them and row
+// kernels under programmatic dependent launch stopped for good when row CTAs that
+// waited for a tensor-core kernel shared its SMs (TMEM is allocated by an
+// instruction that blocks, and a CTA pair needs two SMs at once).
 #pragma once
 
 #include <cuda.h>
@@ -388,8 +394,6 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_mma(const __grid_constant__ 
     }
     if (warp == 2) tmem_alloc<CG>(s_tmem, 512);
     if (warp == 3 && lane < 2) prefetch_map(lane ? &a.tx : &a.tw);
-    pdl_wait();
-    pdl_trigger();
     for (int i = threadIdx.x; i <= a.E; i += kMmaThreads) s_off[i] = a.offsets ? __ldg(a.offsets + i) : (i ? a.M : 0);
     __syncthreads();
     if (warp == 0) {
@@ -594,8 +598,6 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_split(const __grid_constant_
     while ((int)cols < a.bn) cols *= 2;
     if (warp == 2) tmem_alloc<1>(s_tmem, cols);
     if (warp == 3 && lane < 2) prefetch_map(lane ? &a.tx : &a.tw);
-    pdl_wait();
-    pdl_trigger();
     __syncwarp();
     tc_before();
     __syncthreads();

@@ -63,7 +63,6 @@ struct RowArgs {
 };
 
 constexpr int kRowThreads = 512;        // most threads of a CTA
-constexpr int kRowMaxCols = kRowThreads * 8 * 4;
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
@@ -88,18 +87,6 @@ __device__ __forceinline__ void widen8(const uint4& r, int type, float (&v)[8]) 
     }
 }
 
-// Eight consecutive values from element i (a multiple of 8 from a 16-byte
-// aligned row).
-__device__ __forceinline__ void load8(const void* p, int type, int64_t i, float (&v)[8]) {
-    if (type == ELQ_F32) {
-        const float4 a = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p) + i)[0];
-        const float4 b = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p) + i)[1];
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-        return;
-    }
-    widen8(*reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p) + i), type, v);
-}
 __device__ __forceinline__ void store1(void* p, int type, int64_t i, float v) {
     if (type == ELQ_F32) reinterpret_cast<float*>(p)[i] = v;
     else if (type == ELQ_BF16) reinterpret_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);

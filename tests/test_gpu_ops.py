@@ -207,10 +207,11 @@ def test_combine(O, o, T, k, L):
 
 # ---- norms --------------------------------------------------------------------
 
-# relative error of an fp32 norm's factor 1 / sqrt(mean + eps): the sum of squares of up to 17000 / 512 * ...
-# at most 64 values a thread (one rounding each), 5 shuffles and 16 partial sums, a division and the sum with
-# eps, halved by the root; the root and the reciprocal; then the two products of a value
-RSTD = ((64 + 5 + 16 + 2) / 2 + 2) * U32
+# relative error of an fp32 norm's factor 1 / sqrt(mean + eps): the sum of squares of at most 64 values a
+# thread (one rounding each), 5 shuffles and 16 partial sums, halved by the root; the reciprocal of the length
+# and the fused multiply-add with eps, halved; rsqrtf's 2 ulp, which are 4 of these units.  Then the two
+# products of a value.
+RSTD = ((64 + 5 + 16 + 2) / 2 + 4) * U32
 NORM = RSTD + 2 * U32
 
 
