@@ -25,8 +25,7 @@
  *  - Rows, channels and columns number at most 2^30 each.
  *  - No workspace, no allocation, nothing kept between calls but what elq.h
  *    names; any stream, capturable; calls share nothing on the GPU but the error
- *    word below.  A call's kernel may be launched while the kernel before it on
- *    the stream drains; it touches no memory before that one is complete.
+ *    word below.  One kernel a call.
  *    An output may not overlap an input, except where in-place use is said.
  *  - Every sum runs in a fixed order: the same call gives the same bits.
  *  - Device data out of range (row indices, positions, group offsets) never

@@ -41,13 +41,12 @@ int device_sms() {
     return cache[dev];
 }
 
-// Row kernels and the GEMV are launched so that they may start while the kernel
-// before them on the stream drains (programmatic dependent launch, about 1 us less
-// each): they set themselves up and wait for that kernel's completion before they
-// touch global memory.  Tensor-core kernels (early = false) start after its end, and
-// never let the next one in early.
+// Plain launches: no kernel here starts before the one before it on the stream has
+// ended.  (Under programmatic dependent launch, about 1 us less a call, a chain of
+// row kernels and products stopped for good: row CTAs waiting for a product shared
+// its SMs while its CTAs still allocated TMEM and waited for their cluster.)
 template <typename Args>
-cudaError_t launch(void (*kern)(Args), dim3 grid, dim3 threads, size_t smem, cudaStream_t s, const Args& a, bool early,
+cudaError_t launch(void (*kern)(Args), dim3 grid, dim3 threads, size_t smem, cudaStream_t s, const Args& a,
                    int cluster = 1) {
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof(cfg));
@@ -55,20 +54,12 @@ cudaError_t launch(void (*kern)(Args), dim3 grid, dim3 threads, size_t smem, cud
     cfg.blockDim = threads;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    int n = 0;
-    if (early) {
-        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[n++].val.programmaticStreamSerializationAllowed = 1;
-    }
-    if (cluster > 1) {
-        attr[n].id = cudaLaunchAttributeClusterDimension;
-        attr[n].val.clusterDim.x = cluster;
-        attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
-        ++n;
-    }
-    cfg.attrs = attr;
-    cfg.numAttrs = n;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = cluster;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = cluster > 1 ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
@@ -94,7 +85,7 @@ cudaError_t launch_pipe_t(const RowArgs& a, int threads, int groups, size_t smem
     // as many CTAs as fit, by registers (64 a thread with one chunk, 80 with more) and by shared memory
     const int fit = std::max(1, std::min((VPT == 1 ? 1024 : 768) / (threads * groups), (int)(224 * 1024 / (smem + 2048))));
     const dim3 grid((unsigned)std::min<int64_t>((a.rows + groups - 1) / groups, (int64_t)device_sms() * fit));
-    return launch(k_pipe<OP, VPT, D, XT>, grid, dim3(threads, groups), smem, s, a, true);
+    return launch(k_pipe<OP, VPT, D, XT>, grid, dim3(threads, groups), smem, s, a);
 }
 
 // Rows through shared memory; false where they are too long for it.
@@ -145,7 +136,7 @@ bool launch_pipe(RowArgs a, cudaStream_t s, cudaError_t* e) {
 template <int OP, int VPT, bool VEC>
 cudaError_t launch_rows_t(const RowArgs& a, int threads, cudaStream_t s) {
     const int64_t most = (int64_t)device_sms() * std::max(1, 2048 / threads);
-    return launch(k_rows<OP, VPT, VEC>, dim3((unsigned)std::min<int64_t>(a.rows, most)), threads, 0, s, a, true);
+    return launch(k_rows<OP, VPT, VEC>, dim3((unsigned)std::min<int64_t>(a.rows, most)), threads, 0, s, a);
 }
 
 // k_rows: chunks of a row in registers, as few a thread as 512 threads allow,
@@ -261,7 +252,7 @@ cudaError_t launch_gemv(const Product& p, cudaStream_t s) {
     const int groups = p.offsets ? std::min(p.E, p.M) : 1;
     const int most = std::max(1, 4 * device_sms() / groups);
     const dim3 grid((unsigned)std::min<int64_t>(most, ((int64_t)p.N + per - 1) / per), groups);
-    return launch(k_gemv<KIND, R, U>, grid, 32 * kGemvWarps, 0, s, a, true);
+    return launch(k_gemv<KIND, R, U>, grid, 32 * kGemvWarps, 0, s, a);
 }
 
 // Channels a warp takes at a time (R) and pieces of each in flight (U).  8-bit
@@ -322,7 +313,10 @@ bool mma_args(const Product& p, int cg, MmaArgs& a) {
     return encode(&a.tw, es, 3, p.w, dw, sw, bw) && encode(&a.tx, es, 2, p.x, dx, sx, bx);
 }
 
-// Large shared memory for a kernel, once per device.
+// Large shared memory for a kernel, once per device.  The tensor-core kernels take
+// all of an SM's: TMEM is allocated by an instruction that blocks while another CTA
+// of the SM holds it, and CTAs of a cluster wait for one another, so that two such
+// kernels on two streams, sharing SMs, could wait in a circle.
 template <typename K>
 bool mma_optin(K kern, bool* done) {
     int dev = 0;
@@ -346,7 +340,7 @@ elq_status launch_mma(const Product& p, cudaStream_t s) {
     const int hdr = kMmaHdr + 2 * (p.E + 1) * 4 + 1024, stage = kABytes + a.bn / CG * kStepBytes;
     a.stages = std::min(kMmaStagesMax, (kMmaSmemMax - hdr) / stage);
     const dim3 grid((unsigned)std::min<int64_t>(sms, units * CG));
-    return status_of(launch(k_mma<KIND, CG>, grid, kMmaThreads, (size_t)(hdr + a.stages * stage), s, a, false, CG));
+    return status_of(launch(k_mma<KIND, CG>, grid, kMmaThreads, kMmaSmemMax, s, a, CG));
 }
 
 // CTAs per tile and rows of a tile for a dense product split over K; 1 where no
@@ -385,9 +379,8 @@ elq_status launch_split(const Product& p, int split, int bn, cudaStream_t s) {
     a.bn = bn;
     a.split = split;
     a.stages = std::min({kMmaStagesMax, (kMmaSmemMax - hdr) / stage, share});
-    const int smem = hdr + std::max(a.stages * stage, bn * kTileCh * 4);
     const int64_t tiles = (p.M + bn - 1) / bn * (((int64_t)p.N + kTileCh - 1) / kTileCh);
-    return status_of(launch(k_split<KIND>, dim3((unsigned)(tiles * split)), kMmaThreads, smem, s, a, false, split));
+    return status_of(launch(k_split<KIND>, dim3((unsigned)(tiles * split)), kMmaThreads, kMmaSmemMax, s, a, split));
 }
 
 // Pairs of CTAs where their tiles (an expert with rows has one at least) fill the

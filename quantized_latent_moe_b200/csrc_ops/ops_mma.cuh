@@ -15,12 +15,6 @@
 // (channels) it may, 32 rows at a time, rescales, and writes.  Rows of a copied
 // box that belong to the next group, or lie past the matrix (zeros), only meet
 // accumulator columns that are not written.
-//
-// These kernels overlap with no other: they are launched plainly, and let the
-// kernel after them start no earlier than their end.  A chain of them and row
-// kernels under programmatic dependent launch stopped for good when row CTAs that
-// waited for a tensor-core kernel shared its SMs (TMEM is allocated by an
-// instruction that blocks, and a CTA pair needs two SMs at once).
 #pragma once
 
 #include <cuda.h>
@@ -592,11 +586,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_split(const __grid_constant_
         *abort_v = 0;
         fence_barrier_init();
     }
-    // as many TMEM columns as the tile has: the CTAs that fit an SM by shared memory
-    // must all get theirs, or clusters that share SMs could wait for one another
-    uint32_t cols = 32;
-    while ((int)cols < a.bn) cols *= 2;
-    if (warp == 2) tmem_alloc<1>(s_tmem, cols);
+    if (warp == 2) tmem_alloc<1>(s_tmem, 256);
     if (warp == 3 && lane < 2) prefetch_map(lane ? &a.tx : &a.tw);
     __syncwarp();
     tc_before();
@@ -677,7 +667,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_split(const __grid_constant_
     tc_before();
     cluster_sync();         // all partials are there
     tc_after();
-    if (warp == 2) tmem_free<1>(tmem, cols);
+    if (warp == 2) tmem_free<1>(tmem, 256);
     // this CTA's rows: a warp one row, a lane four channels
     const int r0 = rows * rank / S, r1 = rows * (rank + 1) / S, ch = ch0 + 4 * lane;
     float sw[4] = {1.0f, 1.0f, 1.0f, 1.0f}, bias[4] = {0.0f, 0.0f, 0.0f, 0.0f};

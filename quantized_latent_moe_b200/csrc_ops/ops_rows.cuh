@@ -23,12 +23,8 @@
 #include <stdint.h>
 
 #include "../../include/elq_ops.h"
-#include "../csrc/elq_device.cuh"
 
 namespace elqops {
-
-using elq::pdl_trigger;
-using elq::pdl_wait;
 
 enum RowOp { ROW_QUANT = 0, ROW_SWIGLU = 1, ROW_COMBINE = 2, ROW_RMS = 3, ROW_RESIDUAL = 4 };
 
@@ -541,8 +537,6 @@ template <int OP, int VPT, bool VEC>
 __global__ void __launch_bounds__(kRowThreads, VPT == 1 && OP != ROW_COMBINE ? 2 : 1) k_rows(const __grid_constant__ RowArgs a) {
     __shared__ __align__(16) uint32_t red[2][16];
     RowReduce<false> rr(red);
-    pdl_wait();
-    pdl_trigger();
     const int nch = (int)((a.cols + 8ll * blockDim.x - 1) / (8ll * blockDim.x));      // chunks of a thread
     constexpr int NV = VPT > 0 ? VPT : 1, B = VPT == 1 ? 8 : VPT == 2 ? 4 : 2;
     const bool codes = a.n_type == ELQ_I8;
@@ -833,8 +827,6 @@ __global__ void __launch_bounds__(VPT == 1 ? kRowThreads : kPipeThreads4, 2) k_p
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 
-    pdl_wait();
-    pdl_trigger();
     int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     const int64_t step = (int64_t)gridDim.x * blockDim.y;
     const float* w_last = OP == ROW_RMS ? a.w : a.n ? a.w_next : nullptr;     // of the norm that is written

@@ -525,6 +525,57 @@ def test_captured_and_replayed(O, T):
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+def test_chains_of_calls(O):
+    """Bursts of calls with nothing between them (gathered rows to codes, then the product that reads
+    them; buffers come back from the allocator at once) give every time what the first call gave.  Rows
+    of odd width and ragged experts on pairs of CTAs stopped such a chain when its kernels overlapped."""
+    cases = []
+    for T, k, E, N, K in ((647, 2, 128, 675, 1217), (33, 1, 8, 1073, 357), (300, 8, 32, 512, 256)):
+        g = rng(T)
+        idx = torch.rand(T, E, generator=g, device="cuda").topk(k, dim=1).indices.reshape(-1)
+        perm = torch.argsort(idx, stable=True).to(torch.int32)
+        off = torch.searchsorted(idx.sort().values, torch.arange(E + 1, device="cuda")).to(torch.int32)
+        x, (w, sw) = randn(g, T, K, dtype=torch.bfloat16), codes(g, E, N, K)
+        cases.append(lambda x=x, w=w, sw=sw, off=off, perm=perm, k=k: O.grouped_matmul(
+            O.quantize_i8(x, index=perm, index_div=k), O.I8Rows(w, sw * 2.0 ** -12), off, out_dtype=torch.float16))
+    for T, N, K in ((77, 517, 1003), (300, 700, 130), (2048, 1792, 512)):
+        g = rng(T)
+        x, (w, sw) = randn(g, T, K), codes(g, N, K)
+        cases.append(lambda x=x, w=w, sw=sw: O.i8_matmul(O.quantize_i8(x), O.I8Rows(w, sw)))
+    for call in cases:
+        want = call()
+        torch.cuda.synchronize()
+        for burst in (8, 8, 8, 300):
+            for _ in range(burst):
+                y = call()
+            torch.cuda.synchronize()
+            assert torch.equal(y, want)
+    assert O.status() == 0
+
+
+def test_two_streams_at_once(O):
+    """Products on two streams at once: pairs of CTAs against clusters that split K, and both against row
+    kernels, each giving what it gives alone."""
+    g = rng(77)
+    x, w = O.quantize_i8(randn(g, 2048, 1024)), O.quantize_i8(randn(g, 2048, 1024))
+    xs, ws = randn(g, 40, 2048), O.quantize_i8(randn(g, 1000, 2048))
+    big = lambda: O.i8_matmul(x, w, out_dtype=torch.bfloat16)
+    small = lambda: O.i8_matmul(O.quantize_i8(xs), ws)
+    want = big(), small()
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got = [[], []]
+        for i in range(10):
+            for j, call in enumerate((big, small)):
+                with torch.cuda.stream(streams[j]):
+                    got[j].append(call())
+        torch.cuda.synchronize()
+        for j in range(2):
+            assert all(torch.equal(y, want[j]) for y in got[j])
+    assert O.status() == 0
+
+
 def test_stream_argument(O):
     st = torch.cuda.Stream()
     g = rng(8)
