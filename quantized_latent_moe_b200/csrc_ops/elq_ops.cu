@@ -41,12 +41,15 @@ int device_sms() {
     return cache[dev];
 }
 
-// Plain launches: no kernel here starts before the one before it on the stream has
-// ended.  (Under programmatic dependent launch, about 1 us less a call, a chain of
-// row kernels and products stopped for good: row CTAs waiting for a product shared
-// its SMs while its CTAs still allocated TMEM and waited for their cluster.)
+// A product (early) may start while the row kernel before it drains: it sets itself
+// up, and waits for that kernel's completion before it touches global memory.  Only
+// this edge is programmatic.  Row kernels are launched plainly, so that no CTA of
+// theirs ever waits on an SM, and products let nothing start before their end: with
+// both, a chain of row kernels and products stopped for good (row CTAs that waited
+// for a product shared its SMs while its CTAs still allocated TMEM and waited for
+// their cluster).
 template <typename Args>
-cudaError_t launch(void (*kern)(Args), dim3 grid, dim3 threads, size_t smem, cudaStream_t s, const Args& a,
+cudaError_t launch(void (*kern)(Args), dim3 grid, dim3 threads, size_t smem, cudaStream_t s, const Args& a, bool early,
                    int cluster = 1) {
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof(cfg));
@@ -54,12 +57,20 @@ cudaError_t launch(void (*kern)(Args), dim3 grid, dim3 threads, size_t smem, cud
     cfg.blockDim = threads;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = cluster;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = cluster > 1 ? 1 : 0;
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    if (early) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (cluster > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = cluster;
+        attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
     return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
@@ -85,7 +96,7 @@ cudaError_t launch_pipe_t(const RowArgs& a, int threads, int groups, size_t smem
     // as many CTAs as fit, by registers (64 a thread with one chunk, 80 with more) and by shared memory
     const int fit = std::max(1, std::min((VPT == 1 ? 1024 : 768) / (threads * groups), (int)(224 * 1024 / (smem + 2048))));
     const dim3 grid((unsigned)std::min<int64_t>((a.rows + groups - 1) / groups, (int64_t)device_sms() * fit));
-    return launch(k_pipe<OP, VPT, D, XT>, grid, dim3(threads, groups), smem, s, a);
+    return launch(k_pipe<OP, VPT, D, XT>, grid, dim3(threads, groups), smem, s, a, false);
 }
 
 // Rows through shared memory; false where they are too long for it.
@@ -136,7 +147,7 @@ bool launch_pipe(RowArgs a, cudaStream_t s, cudaError_t* e) {
 template <int OP, int VPT, bool VEC>
 cudaError_t launch_rows_t(const RowArgs& a, int threads, cudaStream_t s) {
     const int64_t most = (int64_t)device_sms() * std::max(1, 2048 / threads);
-    return launch(k_rows<OP, VPT, VEC>, dim3((unsigned)std::min<int64_t>(a.rows, most)), threads, 0, s, a);
+    return launch(k_rows<OP, VPT, VEC>, dim3((unsigned)std::min<int64_t>(a.rows, most)), threads, 0, s, a, false);
 }
 
 // k_rows: chunks of a row in registers, as few a thread as 512 threads allow,
@@ -252,7 +263,7 @@ cudaError_t launch_gemv(const Product& p, cudaStream_t s) {
     const int groups = p.offsets ? std::min(p.E, p.M) : 1;
     const int most = std::max(1, 4 * device_sms() / groups);
     const dim3 grid((unsigned)std::min<int64_t>(most, ((int64_t)p.N + per - 1) / per), groups);
-    return launch(k_gemv<KIND, R, U>, grid, 32 * kGemvWarps, 0, s, a);
+    return launch(k_gemv<KIND, R, U>, grid, 32 * kGemvWarps, 0, s, a, true);
 }
 
 // Channels a warp takes at a time (R) and pieces of each in flight (U).  8-bit
@@ -340,7 +351,7 @@ elq_status launch_mma(const Product& p, cudaStream_t s) {
     const int hdr = kMmaHdr + 2 * (p.E + 1) * 4 + 1024, stage = kABytes + a.bn / CG * kStepBytes;
     a.stages = std::min(kMmaStagesMax, (kMmaSmemMax - hdr) / stage);
     const dim3 grid((unsigned)std::min<int64_t>(sms, units * CG));
-    return status_of(launch(k_mma<KIND, CG>, grid, kMmaThreads, kMmaSmemMax, s, a, CG));
+    return status_of(launch(k_mma<KIND, CG>, grid, kMmaThreads, kMmaSmemMax, s, a, true, CG));
 }
 
 // CTAs per tile and rows of a tile for a dense product split over K; 1 where no
@@ -380,7 +391,7 @@ elq_status launch_split(const Product& p, int split, int bn, cudaStream_t s) {
     a.split = split;
     a.stages = std::min({kMmaStagesMax, (kMmaSmemMax - hdr) / stage, share});
     const int64_t tiles = (p.M + bn - 1) / bn * (((int64_t)p.N + kTileCh - 1) / kTileCh);
-    return status_of(launch(k_split<KIND>, dim3((unsigned)(tiles * split)), kMmaThreads, kMmaSmemMax, s, a, split));
+    return status_of(launch(k_split<KIND>, dim3((unsigned)(tiles * split)), kMmaThreads, kMmaSmemMax, s, a, true, split));
 }
 
 // Pairs of CTAs where their tiles (an expert with rows has one at least) fill the

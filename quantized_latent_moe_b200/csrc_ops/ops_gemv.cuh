@@ -208,6 +208,7 @@ __device__ __forceinline__ bool find_group(const int32_t* offsets, int E, int M,
 
 template <int KIND, int R, int U>
 __global__ void __launch_bounds__(32 * kGemvWarps) k_gemv(const __grid_constant__ GemvArgs a) {
+    pdl_wait();
     int e = 0, r0 = 0, r1 = a.M;        // at most min(E, M) groups have rows, and the grid has that many
     if (a.offsets && !find_group(a.offsets, a.E, a.M, blockIdx.y, e, r0, r1)) return;
     const uint8_t* w = a.w + (int64_t)e * a.w_stride;

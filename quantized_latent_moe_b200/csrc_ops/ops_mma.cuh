@@ -388,6 +388,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_mma(const __grid_constant__ 
     }
     if (warp == 2) tmem_alloc<CG>(s_tmem, 512);
     if (warp == 3 && lane < 2) prefetch_map(lane ? &a.tx : &a.tw);
+    pdl_wait();
     for (int i = threadIdx.x; i <= a.E; i += kMmaThreads) s_off[i] = a.offsets ? __ldg(a.offsets + i) : (i ? a.M : 0);
     __syncthreads();
     if (warp == 0) {
@@ -588,6 +589,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_split(const __grid_constant_
     }
     if (warp == 2) tmem_alloc<1>(s_tmem, 256);
     if (warp == 3 && lane < 2) prefetch_map(lane ? &a.tx : &a.tw);
+    pdl_wait();
     __syncwarp();
     tc_before();
     __syncthreads();

@@ -23,8 +23,12 @@
 #include <stdint.h>
 
 #include "../../include/elq_ops.h"
+#include "../csrc/elq_device.cuh"
 
 namespace elqops {
+
+using elq::pdl_trigger;
+using elq::pdl_wait;
 
 enum RowOp { ROW_QUANT = 0, ROW_SWIGLU = 1, ROW_COMBINE = 2, ROW_RMS = 3, ROW_RESIDUAL = 4 };
 
@@ -536,6 +540,7 @@ __device__ __forceinline__ void norm8(const float (&w)[8], float rstd, float (&v
 template <int OP, int VPT, bool VEC>
 __global__ void __launch_bounds__(kRowThreads, VPT == 1 && OP != ROW_COMBINE ? 2 : 1) k_rows(const __grid_constant__ RowArgs a) {
     __shared__ __align__(16) uint32_t red[2][16];
+    pdl_trigger();
     RowReduce<false> rr(red);
     const int nch = (int)((a.cols + 8ll * blockDim.x - 1) / (8ll * blockDim.x));      // chunks of a thread
     constexpr int NV = VPT > 0 ? VPT : 1, B = VPT == 1 ? 8 : VPT == 2 ? 4 : 2;
@@ -827,6 +832,7 @@ __global__ void __launch_bounds__(VPT == 1 ? kRowThreads : kPipeThreads4, 2) k_p
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 
+    pdl_trigger();
     int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     const int64_t step = (int64_t)gridDim.x * blockDim.y;
     const float* w_last = OP == ROW_RMS ? a.w : a.n ? a.w_next : nullptr;     // of the norm that is written
