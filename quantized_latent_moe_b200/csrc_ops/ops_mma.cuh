@@ -158,6 +158,11 @@ __device__ __forceinline__ uint32_t in_cta(const void* p, int rank) {
     return r;
 }
 __device__ __forceinline__ uint32_t first_cta(const void* p) { return in_cta(p, 0); }
+// An arrival on another CTA's barrier that publishes nothing but itself: a release
+// at cluster scope would wait for the outputs just stored to reach L2.
+__device__ __forceinline__ void bar_arrive_remote(uint32_t bar) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
 __device__ __forceinline__ void bar_arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -537,7 +542,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_mma(const __grid_constant__ 
             __syncwarp();
             if (lane == 0) {
                 if (CG == 1) bar_arrive(tempty + acc);
-                else bar_arrive_cluster(first_cta(tempty + acc));
+                else bar_arrive_remote(first_cta(tempty + acc));
             }
         }
     }
