@@ -785,7 +785,8 @@ __device__ __forceinline__ float sumsq(const f32x2 (&v)[VPT][4]) {
 
 // A CTA works on blockDim.y rows at a time, blockDim.x threads each, which share
 // the weights in shared memory.  D stages: the rows in shared memory per row
-// worked on, D - 1 of them on their way.  XT: x's type, or 0xff: as x_type says.
+// worked on, D - 1 of them on their way.  XT: x's type (a residual norm's: of h and n too), or
+// 0xff: as the arguments say.
 constexpr int kAnyType = 0xff;
 constexpr int kPipeThreads4 = 384;     // most threads with four chunks each
 
@@ -793,13 +794,13 @@ template <int OP, int VPT, int D, int XT>
 __global__ void __launch_bounds__(VPT == 1 ? kRowThreads : kPipeThreads4, 2) k_pipe(const __grid_constant__ RowArgs a) {
     extern __shared__ uint4 sm[];
     __shared__ __align__(16) uint32_t red[2 * kRowGroups][16];
-    const int T = blockDim.x, xt = XT == kAnyType ? a.x_type : XT, ht = a.h_type;
+    const int T = blockDim.x, xt = XT == kAnyType ? a.x_type : XT, ht = OP == ROW_RESIDUAL && XT != kAnyType ? XT : a.h_type, nt = OP == ROW_RESIDUAL && XT != kAnyType ? XT : a.n_type;
     Lane<VPT> ln;
     ln.row_bytes16 = 16 * T;
     ln.first = (uint32_t)__cvta_generic_to_shared(sm) + 16 * threadIdx.x;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) ln.nv[i] = min(8, max(0, a.cols - 8 * ((int)threadIdx.x + i * T)));
-    const bool codes = a.n_type == ELQ_I8;
+    const bool codes = nt == ELQ_I8;
     const bool gate_all = OP == ROW_RESIDUAL && a.gate && a.gate_cols > 1 && a.gate_rows >= a.rows;
     const bool gate_row = OP == ROW_RESIDUAL && a.gate && a.gate_cols > 1 && a.gate_rows < a.rows;
     const int plane = VPT * 16 * T;         // bytes of one piece of all the CTA's chunks
@@ -807,7 +808,7 @@ __global__ void __launch_bounds__(VPT == 1 ? kRowThreads : kPipeThreads4, 2) k_p
     const uint32_t ring = ln.first + a.w_planes * plane + threadIdx.y * D * stage_bytes;
     const int ox = planes_of(xt) * plane, oh = ox, og = ox + planes_of(ht) * plane;
     const int64_t bx = a.ldx * (xt == ELQ_F32 ? 4 : 2), bh = a.ldh * (ht == ELQ_F32 ? 4 : 2);
-    const int64_t bo = a.ld_out * (ht == ELQ_F32 ? 4 : 2), bn = a.ldn * (codes ? 1 : a.n_type == ELQ_F32 ? 4 : 2);
+    const int64_t bo = a.ld_out * (ht == ELQ_F32 ? 4 : 2), bn = a.ldn * (codes ? 1 : nt == ELQ_F32 ? 4 : 2);
     const uint8_t* x = reinterpret_cast<const uint8_t*>(a.x);
     const uint8_t* hp = reinterpret_cast<const uint8_t*>(a.h);
     uint8_t* op = reinterpret_cast<uint8_t*>(a.h_out);
@@ -921,7 +922,7 @@ __global__ void __launch_bounds__(VPT == 1 ? kRowThreads : kPipeThreads4, 2) k_p
 #pragma unroll
                     for (int j = 0; j < 4; ++j) v[i][j] = mul2(v[i][j], w[j]);
                 }
-                if (!codes) ln.write(o, i, a.n_type, v[i]);
+                if (!codes) ln.write(o, i, nt, v[i]);
             }
             if (!codes) continue;
         }
