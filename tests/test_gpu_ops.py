@@ -296,6 +296,57 @@ def test_residual_norm_in_place(O):
         assert b.data_ptr() == H.data_ptr() and torch.equal(a, b) and torch.equal(n, m)
 
 
+def test_vectors_off_sixteen_bytes(O):
+    """Weights, gates, bias and scales that start on a 4-byte boundary only."""
+    g = rng(31)
+    C, T = 520, 400
+    off = lambda n: torch.randn(n + 1, generator=g, device="cuda")[1:]
+    H, Y, post, pre, gate = randn(g, T, C), randn(g, T, C, dtype=torch.bfloat16), off(C), off(C), off(C)
+    a = O.residual_norm(H, Y, post, gate=gate, next_weight=pre, next_dtype=torch.bfloat16)
+    v = rms64(Y, post, 1e-6) * gate.double()
+    check(a[0], H.double() + v, NORM * v.abs() + 2 * U32 * (H.double().abs() + v.abs()), torch.float32)
+    ref = rms64(H, post, 1e-6)
+    check(O.rms_norm(H, post), ref, NORM * ref.abs(), torch.float32)
+    for rows in (3, 200):
+        (x, sx), (w, sw) = codes(g, rows, 64), codes(g, 50, 64)
+        sx2, sw2, bias = torch.empty(rows + 1, device="cuda")[1:].copy_(sx), torch.empty(51, device="cuda")[1:].copy_(sw), off(50)
+        y = O.i8_matmul(O.I8Rows(x, sx2), O.I8Rows(w, sw2), bias=bias)
+        ref = product64(x, sx, w, sw)
+        check(y, ref + bias.double(), 3.01 * U32 * ref.abs() + U32 * (ref + bias.double()).abs(), torch.float32)
+
+
+def test_no_rows(O):
+    z = torch.empty(0, 64, device="cuda")
+    w = O.quantize_i8(torch.randn(32, 64, device="cuda"))
+    ws = O.I8Rows(w.q.view(2, 16, 64), w.scale.view(2, 16))
+    assert O.quantize_i8(z).q.shape == (0, 64) and O.swiglu_i8(z).q.shape == (0, 32)
+    assert O.combine_i8(torch.ones(3, 64, device="cuda"), torch.empty(0, dtype=torch.int32, device="cuda"),
+                        torch.empty(0, 2, device="cuda")).q.shape == (0, 64)
+    assert O.rms_norm(z).shape == (0, 64) and O.rms_norm_i8(z).scale.shape == (0,)
+    for gate in (None, torch.ones(64, device="cuda"), torch.ones(0, 64, device="cuda"), torch.ones(0, 1, device="cuda")):
+        h, n = O.residual_norm(z, z.clone(), gate=gate, next_dtype=torch.int8)
+        assert h.shape == (0, 64) and n.q.shape == (0, 64)
+    assert O.i8_matmul(O.quantize_i8(z), w).shape == (0, 32)
+    off = torch.zeros(3, dtype=torch.int32, device="cuda")
+    assert O.grouped_matmul(O.quantize_i8(z), ws, off).shape == (0, 16)
+    assert O.grouped_matmul(z.half(), torch.ones(2, 16, 64, device="cuda").half(), off).shape == (0, 16)
+    torch.cuda.synchronize()
+
+
+def test_single_expert_and_single_columns(O):
+    g = rng(41)
+    for M in (1, 7, 50):
+        (x, sx), (w, sw) = codes(g, M, 33), codes(g, 1, 70, 33)
+        y = O.grouped_matmul(O.I8Rows(x, sx), O.I8Rows(w, sw), offsets_of([M]))
+        ref = product64(x, sx, w[0], sw[0])
+        check(y, ref, 3.01 * U32 * ref.abs(), torch.float32)
+        assert torch.equal(y, O.i8_matmul(O.I8Rows(x, sx), O.I8Rows(w[0], sw[0])))
+        (x, sx), (w, sw) = codes(g, M, 1), codes(g, 4, 1, 1)
+        y = O.grouped_matmul(O.I8Rows(x, sx), O.I8Rows(w, sw), offsets_of([0, M // 2, 0, M - M // 2]))
+        ref = torch.cat([product64(x[:M // 2], sx[:M // 2], w[1], sw[1]), product64(x[M // 2:], sx[M // 2:], w[3], sw[3])])
+        check(y, ref, 3.01 * U32 * ref.abs(), torch.float32)
+
+
 # ---- products -----------------------------------------------------------------
 
 def product64(q, s, w, sw):
