@@ -20,7 +20,7 @@ namespace {
 PyObject* g_error = nullptr;            // elq.ElqError
 PyObject* g_memory = nullptr;           // torch.OutOfMemoryError
 PyTypeObject* g_rows = nullptr;         // ops.I8Rows
-PyObject *s_q, *s_scale, *s_buf, *s_rows, *s_cols, *s_ld;
+PyObject *s_q, *s_scale, *s_buf, *s_cols;
 
 struct Refused {};                      // a Python exception is set
 
@@ -134,11 +134,11 @@ Rows rows_of(PyObject* o, const char* what, int dev) {
         r.m.type = ELQ_I8;
         r.m.dev = (int)b.get_device();
         check(dev < 0 || r.m.dev == dev, what);
-        Owned n(attr(o, s_rows)), c(attr(o, s_cols)), l(attr(o, s_ld));
-        r.m.rows = number(n.o);
+        Owned c(attr(o, s_cols));
         r.m.cols = number(c.o);
-        r.m.ld = number(l.o);
-        check(b.numel() >= r.m.rows * (r.m.ld + 4), what);
+        check(r.m.cols >= 1, what);
+        r.m.ld = padded(r.m.cols);
+        r.m.rows = b.numel() / (r.m.ld + 4);
         r.m.p = b.data_ptr();
         r.scale = reinterpret_cast<const float*>(static_cast<char*>(r.m.p) + r.m.rows * r.m.ld);
         return r;
@@ -213,7 +213,8 @@ struct On {
     }
 };
 
-// New codes: a buffer of rows padded to 16 bytes, then the scales.
+// New codes: a buffer of rows padded to 16 bytes, then the scales (so that its size
+// and the columns say the rest).
 struct NewRows {
     at::Tensor buf;
     int64_t rows, cols, ld;
@@ -227,11 +228,9 @@ struct NewRows {
     PyObject* object() {
         PyObject* o = g_rows->tp_alloc(g_rows, 0);
         if (!o) throw Refused();
-        Owned b(THPVariable_Wrap(std::move(buf))), n(PyLong_FromLongLong(rows)), c(PyLong_FromLongLong(cols)),
-            l(PyLong_FromLongLong(ld));
-        if (!b.o || !n.o || !c.o || !l.o || PyObject_SetAttr(o, s_q, Py_None) || PyObject_SetAttr(o, s_scale, Py_None) ||
-            PyObject_SetAttr(o, s_buf, b.o) || PyObject_SetAttr(o, s_rows, n.o) || PyObject_SetAttr(o, s_cols, c.o) ||
-            PyObject_SetAttr(o, s_ld, l.o)) {
+        Owned b(THPVariable_Wrap(std::move(buf))), c(PyLong_FromLongLong(cols));
+        if (!b.o || !c.o || PyObject_SetAttr(o, s_q, Py_None) || PyObject_SetAttr(o, s_scale, Py_None) ||
+            PyObject_SetAttr(o, s_buf, b.o) || PyObject_SetAttr(o, s_cols, c.o)) {
             Py_DECREF(o);
             throw Refused();
         }
@@ -504,8 +503,6 @@ PyMODINIT_FUNC PyInit__ops(void) {
     s_q = PyUnicode_InternFromString("_q");
     s_scale = PyUnicode_InternFromString("_scale");
     s_buf = PyUnicode_InternFromString("_buf");
-    s_rows = PyUnicode_InternFromString("_rows");
     s_cols = PyUnicode_InternFromString("_cols");
-    s_ld = PyUnicode_InternFromString("_ld");
     return PyModule_Create(&g_module);
 }

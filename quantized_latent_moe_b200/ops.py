@@ -70,21 +70,28 @@ class I8Rows:
     Rows that a call here made lie in one buffer, the codes, then the scales; q
     and scale are views of it, made when asked for."""
 
-    __slots__ = ("_q", "_scale", "_buf", "_rows", "_cols", "_ld")
+    __slots__ = ("_q", "_scale", "_buf", "_cols")
 
     def __init__(self, q: torch.Tensor, scale: torch.Tensor):
         self._q, self._scale, self._buf = q, scale, None
 
+    def _layout(self):
+        """Rows, and bytes between them, in the buffer."""
+        ld = (self._cols + 15) // 16 * 16
+        return self._buf.numel() // (ld + 4), ld
+
     @property
     def q(self) -> torch.Tensor:
         if self._q is None:
-            self._q = self._buf.as_strided((self._rows, self._cols), (self._ld, 1))
+            rows, ld = self._layout()
+            self._q = self._buf.as_strided((rows, self._cols), (ld, 1))
         return self._q
 
     @property
     def scale(self) -> torch.Tensor:
         if self._scale is None:
-            self._scale = self._buf[self._rows * self._ld:].view(torch.float32)
+            rows, ld = self._layout()
+            self._scale = self._buf[rows * ld:].view(torch.float32)
         return self._scale
 
     @property
@@ -133,7 +140,8 @@ def quantize_i8(x: torch.Tensor, index: torch.Tensor | None = None, index_div: i
     if index is None and isinstance(x, torch.Tensor) and x.dim() == 3 and x.is_contiguous():
         E, N, K = x.shape
         r = (_N or _native()).quantize_i8(x.view(E * N, K), None, 1)
-        return I8Rows(r._buf.as_strided((E, N, K), (N * r._ld, r._ld, 1)), r.scale.view(E, N))
+        ld = r._layout()[1]
+        return I8Rows(r._buf.as_strided((E, N, K), (N * ld, ld, 1)), r.scale.view(E, N))
     return (_N or _native()).quantize_i8(x, index, index_div)
 
 
