@@ -199,10 +199,13 @@ __device__ __forceinline__ int code_of(float x, const CodeScale& c) {
 // compared with half a scale all eight at once, and only eight that have one at
 // or past it are settled one by one.  (bf16 rows have such border cases: half of
 // a row's largest value is 63.5 scales, and about one value in a thousand is it.)
+// PLAIN: the row's scale is a normal one (plain_scale).
+__device__ __forceinline__ bool plain_scale(const CodeScale& c) { return c.up == 1.0f && c.inv != 0.0f; }
+
+template <bool PLAIN>
 __device__ __forceinline__ uint2 codes8(const f32x2 (&v)[4], const CodeScale& c) {
-    if (c.inv == 0.0f) return make_uint2(0, 0);
     uint32_t b[8];
-    if (c.up == 1.0f) {
+    if constexpr (PLAIN) {
         const f32x2 magic = pair(12582912.0f, 12582912.0f), inv = pair(c.inv, c.inv), sm = pair(c.sm, c.sm);
         float worst = 0.0f;
         f32x2 r[4];
@@ -380,7 +383,7 @@ __device__ __forceinline__ void put_codes8(int8_t* q, int64_t row0, int i, int c
     if (VEC && elem<VEC>(i, 0) + 8 <= cols) {
         f32x2 p[4];
         pairs8(v, p);
-        *reinterpret_cast<uint2*>(q + row0 + elem<VEC>(i, 0)) = codes8(p, cs);
+        *reinterpret_cast<uint2*>(q + row0 + elem<VEC>(i, 0)) = plain_scale(cs) ? codes8<true>(p, cs) : codes8<false>(p, cs);
         return;
     }
 #pragma unroll
@@ -536,9 +539,10 @@ __device__ __forceinline__ void norm8(const float (&w)[8], float rstd, float (&v
 }
 
 // VPT: chunks a thread holds in registers (VPT * blockDim.x >= ceil(cols / 8)),
-// or 0: none, every step reads its inputs again.
+// or 0: none, every step reads its inputs again.  With one chunk a thread the row
+// kernels are short of warps, not of registers: 56 leave 1152 threads an SM.
 template <int OP, int VPT, bool VEC>
-__global__ void __launch_bounds__(kRowThreads, VPT == 1 && OP != ROW_COMBINE ? 2 : 1) k_rows(const __grid_constant__ RowArgs a) {
+__global__ void __maxnreg__(VPT == 1 && OP != ROW_COMBINE ? 56 : 128) k_rows(const __grid_constant__ RowArgs a) {
     __shared__ __align__(16) uint32_t red[2][16];
     pdl_trigger();
     RowReduce<false> rr(red);
@@ -758,9 +762,10 @@ struct Lane {
                 if (j < nv[i]) store1(dst, type, e0 + j, v[j]);
         }
     }
+    template <bool PLAIN>
     __device__ __forceinline__ void write_codes(int8_t* dst, int i, const f32x2 (&v)[4], const CodeScale& cs) const {
         const int e0 = 8 * threadIdx.x + i * (row_bytes16 >> 1);
-        const uint2 w = codes8(v, cs);
+        const uint2 w = codes8<PLAIN>(v, cs);
         if (nv[i] == 8) {
             *reinterpret_cast<uint2*>(dst + e0) = w;
         } else {
@@ -931,8 +936,13 @@ __global__ void __launch_bounds__(VPT == 1 ? kRowThreads : kPipeThreads4, 2) k_p
         for (int i = 0; i < VPT; ++i) m = amax8(m, v[i]);
         const CodeScale cs = code_scale(rr.max(__float_as_uint(m)));
         int8_t* q = reinterpret_cast<int8_t*>(np) + row * bn;
+        if (plain_scale(cs)) {
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) ln.write_codes(q, i, v[i], cs);
+            for (int i = 0; i < VPT; ++i) ln.template write_codes<true>(q, i, v[i], cs);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) ln.template write_codes<false>(q, i, v[i], cs);
+        }
         if (threadIdx.x == 0) a.scale[row] = cs.s;
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
