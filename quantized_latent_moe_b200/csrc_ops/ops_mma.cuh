@@ -15,6 +15,12 @@
 // (channels) it may, 32 rows at a time, rescales, and writes.  Rows of a copied
 // box that belong to the next group, or lie past the matrix (zeros), only meet
 // accumulator columns that are not written.
+//
+// Bound by the weights' HBM traffic where groups are small, by L2 to shared memory
+// and the tensor cores (and power) where rows are many.  Measured on B200: 256 rows
+// over 128 experts of 2048 x 1792 codes 75 us (6.3 TB/s), 16384 rows 95 us (5.9
+// TB/s; bf16, 1792 x 1024: 96 us), dense 8192 x 4096 x 4096 codes 85 us (3.2 POP/s,
+// of 4.58 that MMAs alone reach).
 #pragma once
 
 #include <cuda.h>

@@ -15,6 +15,11 @@
 //           many independent loads), unaligned rows (element by element), and
 //           rows longer than a CTA's registers hold, which take the same steps
 //           but read their inputs again for each.
+//
+// Measured on B200: 8192 x 4096 bf16 to codes 21 us (4.8 TB/s), 16384 gathered rows
+// of 1792 22.6, SwiGLU of 16384 x 2048 18.5 (4.5 TB/s), norm of 2048 x 4096 bf16 12,
+// residual norm with the next norm 18.5 (3.6 TB/s); one row of 4096 2 to 5 us.  For
+// many rows instruction issue is what keeps them from HBM speed.
 #pragma once
 
 #include <cuda_bf16.h>
