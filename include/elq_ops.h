@@ -68,8 +68,9 @@ elq_status elq_quantize_i8(const void* x, int32_t x_type, int64_t x_rows, int32_
                            float* scale, void* stream);
 
 /* SwiGLU, then the row quantiser: row i of gu is I gate values, then I up
- * values (ld >= 2 I); h = (g / (1 + exp(-g))) * u in fp32, within 2^-21 of its
- * value (or 2^-118 |u|, where g < -87), quantised to q [rows][I] and scale [rows]. */
+ * values (ld >= 2 I); h = (g / (1 + exp(-g))) * u in fp32, within 5 * 2^-24 of its
+ * value (or 2^-119 |u| where g < -87, or 2^-149), quantised to q [rows][I] and scale
+ * [rows]. */
 elq_status elq_swiglu_i8(const void* gu, int32_t x_type, int64_t rows, int32_t I, int64_t ld, int8_t* q,
                          int64_t ldq, float* scale, void* stream);
 

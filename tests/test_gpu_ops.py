@@ -181,6 +181,28 @@ def test_swiglu(O, x, T, I, pad):
     check_codes(O.swiglu_i8(gu), v, err)
 
 
+@pytest.mark.parametrize("I", [1, 8])
+def test_swiglu_value(O, I):
+    """The value itself, over all of g's range: a row of one value (or eight alike, which go the aligned way)
+    has the scale |h| / 127, so that |h| shows to within that division's rounding."""
+    g = rng(3)
+    gate = torch.cat([torch.linspace(-88.7, 88.7, 1 << 19, device="cuda"), torch.randn(1 << 19, generator=g, device="cuda")])
+    up = torch.exp2(torch.rand(gate.numel(), generator=g, device="cuda") * 8 - 4)
+    r = O.swiglu_i8(torch.cat([gate[:, None].expand(-1, I), up[:, None].expand(-1, I)], 1).contiguous())
+    ref = gate.double() / (1 + torch.exp(-gate.double())) * up.double()
+    # exp within an ulp (two units of 2^-24) and by its share of the sum; the sum, the quotient, the product; then the
+    # scale's division, whose half step is 2^-150 where it is subnormal.  Zero is allowed below exp's range.
+    share = torch.sigmoid(-gate.double())
+    tol = (2 * share + 3 + 1) * U32 * (1 + 2.0 ** -16) * ref.abs() + 127 * 2.0 ** -150
+    tol = tol + torch.where(gate < -87, 2.0 ** -119, 0.0) * up.double()
+    off = (r.scale.double() * 127 - ref.abs()).abs()
+    assert bool((off <= tol).all()), "%d of %d over" % (int((off > tol).sum()), off.numel())
+    # the steps themselves: torch's exp is CUDA's too, and a quotient good to 2^-45 before its rounding is rounded
+    # as the exact one but for 2^-20 of them
+    steps = (gate / (1 + torch.exp(-gate)) * up).abs()[gate > -87]
+    assert int((r.scale[gate > -87] != (steps.double() / 127).float()).sum()) <= gate.numel() // 1000
+
+
 def test_swiglu_nonfinite(O):
     gu = torch.randn(4, 128, generator=rng(1), device="cuda")
     gu[1, 3], gu[2, 70], gu[3, 0] = float("nan"), float("inf"), float("-inf")
