@@ -86,7 +86,8 @@ elq_status elq_combine_i8(const void* o, int32_t o_type, int64_t o_rows, int32_t
 /* ---- products -------------------------------------------------------------------- */
 
 /* y[t][n] = (sum_k x[t][k] * w[n][k]) * sx[t] * sw[n] (+ bias[n]): 8-bit codes,
- * an exact int32 sum, one scale a token and one a channel.  x: device int8
+ * an exact int32 sum, one scale a token and one a channel (in this order, each
+ * operation one fp32 rounding, so that all forms of it agree).  x: device int8
  * [T][K]; sx: device fp32 [T]; w: device int8 [N][K]; sw: device fp32 [N];
  * bias: device fp32 [N] or NULL; y: device [T][N], y_type F32, BF16 or F16.
  * ldx and ldw multiples of 16; 1 <= K <= 65536, N >= 1. */

@@ -151,7 +151,7 @@ __device__ __forceinline__ void gemv_rows(const GemvArgs& a, const uint8_t* w, c
     if (lane % per == 0 && n < a.N && t < nt) {
         float v = (float)s;
         if (KIND == KIND_I8) {
-            v = __fmul_rn(__fmul_rn(v, __ldg(sw + n)), __ldg(a.sx + t0 + t));
+            v = __fmul_rn(__fmul_rn(v, __ldg(a.sx + t0 + t)), __ldg(sw + n));
             if (a.bias) v = __fadd_rn(v, __ldg(a.bias + n));
         }
         store1(a.y, a.y_type, (int64_t)(t0 + t) * a.ldy + n, v);

@@ -320,8 +320,8 @@ __device__ __forceinline__ Unit unit_of(int u, const int* s_off, const int* s_ti
 // instructions decides whether they keep up: the output type is chosen once per 32,
 // the rows' scales come four at a time, and a row costs one pointer step.
 
-// The accumulators r of 32 rows as outputs: times the channel's and the rows'
-// scales (codes), plus the bias.
+// The accumulators r of 32 rows as outputs: times the rows' scales, then the
+// channel's (codes), plus the bias.
 template <int KIND>
 __device__ __forceinline__ void scale32(const uint32_t (&r)[32], const float* sx, float sw, float bias, bool add,
                                         float (&v)[32]) {
@@ -333,10 +333,10 @@ __device__ __forceinline__ void scale32(const uint32_t (&r)[32], const float* sx
 #pragma unroll
     for (int j = 0; j < 32; j += 4) {
         const float4 s = *reinterpret_cast<const float4*>(sx + j);
-        v[j] = __fmul_rn(__fmul_rn((float)(int)r[j], sw), s.x);
-        v[j + 1] = __fmul_rn(__fmul_rn((float)(int)r[j + 1], sw), s.y);
-        v[j + 2] = __fmul_rn(__fmul_rn((float)(int)r[j + 2], sw), s.z);
-        v[j + 3] = __fmul_rn(__fmul_rn((float)(int)r[j + 3], sw), s.w);
+        v[j] = __fmul_rn(__fmul_rn((float)(int)r[j], s.x), sw);
+        v[j + 1] = __fmul_rn(__fmul_rn((float)(int)r[j + 1], s.y), sw);
+        v[j + 2] = __fmul_rn(__fmul_rn((float)(int)r[j + 2], s.z), sw);
+        v[j + 3] = __fmul_rn(__fmul_rn((float)(int)r[j + 3], s.w), sw);
     }
     if (add) {
 #pragma unroll
@@ -721,7 +721,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_split(const __grid_constant_
             const float sx = __ldg(a.sx + row0 + r);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                v[j] = __fmul_rn(__fmul_rn((float)t[j], sw[j]), sx);
+                v[j] = __fmul_rn(__fmul_rn((float)t[j], sx), sw[j]);
                 if (a.bias) v[j] = __fadd_rn(v[j], bias[j]);
             }
         } else {

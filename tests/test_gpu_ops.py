@@ -410,6 +410,18 @@ def test_i8_matmul_exact_sums(O):
         assert torch.equal(y.double(), x.double() @ w.double().T)
 
 
+@pytest.mark.parametrize("T,N,K", [(1, 300, 512), (4, 130, 1003), (20, 517, 2048), (300, 300, 256), (2100, 2050, 256)])
+def test_i8_matmul_scales_in_order(O, T, N, K):
+    """((sum * sx) * sw) + bias, each step one fp32 rounding: the same bits from every form of the product."""
+    g = rng(T * N)
+    (x, sx), (w, sw), bias = codes(g, T, K), codes(g, N, K), randn(g, N)
+    s = (x.double() @ w.double().T).float()
+    want = s * sx.unsqueeze(1) * sw + bias
+    assert torch.equal(O.i8_matmul(O.I8Rows(x, sx), O.I8Rows(w, sw), bias=bias), want)
+    y = O.grouped_matmul(O.I8Rows(x, sx), O.I8Rows(w.unsqueeze(0), sw.unsqueeze(0)), offsets_of([T]))
+    assert torch.equal(y, s * sx.unsqueeze(1) * sw)
+
+
 def test_i8_matmul_nan_rows_and_empty(O):
     for T in (6, 60):
         (x, sx), (w, sw) = codes(rng(T), T, 256), codes(rng(9), 200, 256)
