@@ -164,11 +164,6 @@ __device__ __forceinline__ uint32_t in_cta(const void* p, int rank) {
     return r;
 }
 __device__ __forceinline__ uint32_t first_cta(const void* p) { return in_cta(p, 0); }
-// An arrival on another CTA's barrier that publishes nothing but itself: a release
-// at cluster scope would wait for the outputs just stored to reach L2.
-__device__ __forceinline__ void bar_arrive_remote(uint32_t bar) {
-    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
 __device__ __forceinline__ void bar_arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -240,15 +235,32 @@ __host__ __device__ constexpr uint32_t mma_idesc(int kind, int cg) {
                             : (1u << 4) | (kind == KIND_BF16 ? (1u << 7) | (1u << 10) : 0u));
 }
 
+// Whether an mbarrier's phase is over, waiting for it up to hint_ns.  CLUSTER: what threads of the
+// cluster's other CTAs did before they arrived is seen too.
+template <bool CLUSTER>
+__device__ __forceinline__ bool bar_try(uint64_t* bar, uint32_t parity, uint32_t hint_ns) {
+    if constexpr (!CLUSTER) return mbar_try_wait_hint(bar, parity, hint_ns);
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(hint_ns)
+        : "memory");
+    return ok != 0;
+}
+
 // Bounded wait for an mbarrier phase; gives up at once when another role has.  The
 // clock is read only once a wait is long: reading it costs as much as a whole
 // step of the pipeline.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatile int* abort_v) {
     for (int i = 0; i < 32; ++i)
-        if (mbar_try_wait(bar, parity)) return true;
+        if (CLUSTER ? bar_try<true>(bar, parity, 0) : mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = global_timer_ns();
     for (uint32_t i = 0; i < (1u << 26); ++i) {
-        if (mbar_try_wait_hint(bar, parity, 20000u)) return true;
+        if (bar_try<CLUSTER>(bar, parity, 20000u)) return true;
         if (*abort_v) return false;
         if ((i & 15) == 15 && global_timer_ns() - t0 > kOpsWaitNs) break;
     }
@@ -265,16 +277,8 @@ __device__ __forceinline__ void cluster_leave(uint64_t* bye, int n) {
     if ((int)threadIdx.x < n) bar_arrive_cluster(in_cta(bye, threadIdx.x));
     if (threadIdx.x == 0) {
         const uint64_t t0 = global_timer_ns();
-        uint32_t ok = 0;
-        while (!ok) {
-            asm volatile(
-                "{\n\t.reg .pred p;\n\t"
-                "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], 0;\n\t"
-                "selp.u32 %0, 1, 0, p;\n\t}"
-                : "=r"(ok)
-                : "r"(smem_addr(bye))
-                : "memory");
-            if (!ok && global_timer_ns() - t0 > kOpsWaitNs + 10 * kOpsDrainNs) {
+        while (!bar_try<true>(bye, 0, 20000u)) {
+            if (global_timer_ns() - t0 > kOpsWaitNs + 10 * kOpsDrainNs) {
                 atomicExch(&g_ops_err, 2);
                 break;
             }
@@ -375,7 +379,8 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_mma(const __grid_constant__ 
     uint64_t* tempty = tfull + 2;
     uint64_t* drain = tempty + 2;
     uint64_t* bye = drain + 1;
-    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bye + 1);
+    uint64_t* tdone = bye + 1;
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(tdone + 2);
     volatile int* abort_v = reinterpret_cast<volatile int*>(s_tmem + 1);
     float* s_sx = reinterpret_cast<float*>(smem + 512);
     int* s_off = reinterpret_cast<int*>(smem + kMmaHdr);
@@ -390,7 +395,8 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_mma(const __grid_constant__ 
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(tfull + i, 1);
-            mbar_init(tempty + i, kMmaEpiWarps * CG);
+            mbar_init(tempty + i, CG == 1 ? kMmaEpiWarps : 2);
+            mbar_init(tdone + i, kMmaEpiWarps);
         }
         mbar_init(drain, 1);
         mbar_init(bye, CG);
@@ -480,7 +486,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_mma(const __grid_constant__ 
             for (int u = u0; ok && u < units; u += du, ++it) {
                 const Unit x = unit_of<CG>(u, s_off, s_tile, a.E, ch_tiles);
                 const int acc = it & 1;
-                if (!(ok = bar_wait(tempty + acc, ((it >> 1) & 1) ^ 1, abort_v))) break;
+                if (!(ok = bar_wait<CG == 2>(tempty + acc, ((it >> 1) & 1) ^ 1, abort_v))) break;
                 tc_after();
                 const uint32_t idesc = a.idesc | ((uint32_t)(x.n >> 3) << 17), d = tmem + acc * 256;
                 for (int k = 0; k < steps; ++k) {
@@ -510,6 +516,18 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_mma(const __grid_constant__ 
                 }
             }
         }
+    } else if (CG == 2 && warp == 3) {
+        // A pair's accumulators go back to the first CTA, which issues the MMAs, by a release at cluster
+        // scope.  That waits for the outputs stored before it, so this warp, which has nothing else to
+        // do, passes the epilogue's arrivals on (released by the epilogue's warps themselves, 2048 x 1792
+        // x 4096 took 17.1 us, 16.2 so).
+        if (elect_one()) {
+            int it = 0;
+            for (int u = u0; u < units; u += du, ++it) {
+                if (!bar_wait(tdone + (it & 1), (it >> 1) & 1, abort_v)) break;
+                bar_arrive_cluster(first_cta(tempty + (it & 1)));
+            }
+        }
     } else if (warp >= 4) {
         const int q = warp & 3, half = (warp - 4) >> 2;
         float* sx = s_sx + (warp - 4) * 32;
@@ -524,10 +542,18 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_mma(const __grid_constant__ 
             }
             if (!__all_sync(0xffffffffu, bar_wait(tfull + acc, (it >> 1) & 1, abort_v))) break;
             tc_after();
+            // The accumulator goes back as soon as this warp's last values of it are in registers.
+            auto give_back = [&] {
+                tc_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive((CG == 1 ? tempty : tdone) + acc);
+            };
+            if (half * 32 >= x.rows) give_back();
             for (int c = half * 32; c < x.rows; c += 64) {
                 uint32_t r[32];
                 __syncwarp();
                 tmem_read32(tmem + acc * 256 + c + ((uint32_t)(q * 32) << 16), r);
+                if (c + 64 >= x.rows) give_back();
                 const int nr = min(32, x.rows - c);
                 if (KIND == KIND_I8) {
                     __syncwarp();
@@ -543,12 +569,6 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_mma(const __grid_constant__ 
                     else write32(reinterpret_cast<__half*>(a.y) + at, a.ldy, nr, v);
                 }
                 __syncwarp();
-            }
-            tc_before();
-            __syncwarp();
-            if (lane == 0) {
-                if (CG == 1) bar_arrive(tempty + acc);
-                else bar_arrive_remote(first_cta(tempty + acc));
             }
         }
     }

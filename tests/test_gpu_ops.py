@@ -487,6 +487,57 @@ def test_grouped(O, kind, out, N, K, name, counts, lead, tail):
     assert O.status() == 0
 
 
+def pair_tiles(M, N, E=1):
+    """The host's rule: products whose tiles of 256 channels fill the SMs more than once go to pairs of CTAs."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    return -(-N // 256) * max(min(E, M), -(-M // 256)) > sms // 2
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("T,N,K", [(2100, 2050, 1003), (4001, 1300, 272), (700, 7000, 130), (2600, 4096, 1792)])
+def test_pairs_dense(O, out, T, N, K):
+    """Pairs of CTAs: several tiles a pair (accumulators handed back and forth), tiles of up to 256 rows, a bias."""
+    assert pair_tiles(T, N)
+    g = rng(T + K)
+    (x, sx), (w, sw), bias = codes(g, T, K), codes(g, N, K), randn(g, N)
+    sx = sx * 2.0 ** -14
+    buf = torch.full((T, N + 3), GUARD, dtype=DT[out], device="cuda")
+    O.i8_matmul(O.I8Rows(x, sx), O.I8Rows(w, sw), bias=bias, out_dtype=DT[out], out=buf[:, :N])
+    ref = product64(x, sx, w, sw)
+    check(buf[:, :N], ref + bias.double(), 3.01 * U32 * ref.abs() + U32 * (ref + bias.double()).abs(), DT[out])
+    assert bool((buf[:, N:] == GUARD).all()) and O.status() == 0
+
+
+@pytest.mark.parametrize("kind,out", [("i8", "f32"), ("i8", "bf16"), ("i8", "f16"), ("bf16", "bf16"), ("bf16", "f32"), ("f16", "f16")])
+@pytest.mark.parametrize("N,K", [(1000, 1003), (2048, 256)])
+def test_pairs_grouped(O, kind, out, N, K):
+    """Pairs of CTAs on ragged groups: none, one and several row tiles a group, tiles of 32 to 256 rows."""
+    counts = [0, 700, 1, 33, 64, 0, 65, 129, 257, 512, 513, 31, 255, 256, 97, 0, 300, 2, 40, 161]
+    lead, tail, E = 5, 9, len(counts)
+    M = lead + sum(counts) + tail
+    assert pair_tiles(M, N, E)
+    off, g = offsets_of(counts, lead), rng(N + K)
+    rows = slice(lead, M - tail)
+    buf = torch.full((M, N + 1), GUARD, dtype=DT[out], device="cuda")
+    if kind == "i8":
+        (x, sx), (w, sw) = codes(g, M, K), codes(g, E, N, K)
+        sx = sx * 2.0 ** -14
+        O.grouped_matmul(O.I8Rows(x, sx), O.I8Rows(w, sw), off, out_dtype=DT[out], out=buf[:, :N])
+        ref = grouped64(x, w, off) * sx.double().unsqueeze(-1)      # whole numbers below 2^53, then two products
+        ref = ref * torch.cat([sw[0].expand(lead, N)] + [sw[e].expand(c, N) for e, c in enumerate(counts)] +
+                              [sw[0].expand(tail, N)]).double()
+        err = 3.01 * U32 * ref.abs()
+    else:
+        pad = -K % 8
+        x, w = randn(g, M, K, dtype=DT[kind], ld=K + pad), randn(g, E, N, K, dtype=DT[kind], ld=K + pad)
+        O.grouped_matmul(x, w, off, out_dtype=DT[out], out=buf[:, :N])
+        ref = grouped64(x, w, off)
+        err = K * 2.0 ** -23 * grouped64(x.double().abs(), w.double().abs(), off)       # as in test_grouped
+    check(buf[rows, :N], ref[rows], err[rows], DT[out])
+    assert bool((buf[:lead] == GUARD).all()) and bool((buf[M - tail:] == GUARD).all()) and bool((buf[:, N:] == GUARD).all())
+    assert O.status() == 0
+
+
 @pytest.mark.parametrize("M", [6, 300])
 def test_grouped_bad_offsets(O, M):
     """Offsets out of range are clamped, and raised to the largest before them."""
@@ -658,6 +709,30 @@ def test_two_streams_at_once(O):
         torch.cuda.synchronize()
         for j in range(2):
             assert all(torch.equal(y, want[j]) for y in got[j])
+    assert O.status() == 0
+
+
+def test_pairs_on_two_streams(O):
+    """Products on pairs of CTAs on one stream, on the other products of clusters that split K, row kernels, and
+    pairs again: each gives what it gives alone."""
+    g = rng(78)
+    assert pair_tiles(2500, 2304) and not pair_tiles(40, 1000)
+    x, w = O.quantize_i8(randn(g, 2500, 512)), O.quantize_i8(randn(g, 2304, 512))
+    xs, ws = randn(g, 40, 2048), O.quantize_i8(randn(g, 1000, 2048))
+    big = lambda: O.i8_matmul(x, w, out_dtype=torch.bfloat16)
+    calls = [[big], [lambda: O.i8_matmul(O.quantize_i8(xs), ws), big]]
+    want = [[c() for c in cs] for cs in calls]
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got = [[], []]
+        for i in range(10):
+            for j in range(2):
+                with torch.cuda.stream(streams[j]):
+                    got[j].append([c() for c in calls[j]])
+        torch.cuda.synchronize()
+        for j in range(2):
+            assert all(torch.equal(a, b) for ys in got[j] for a, b in zip(ys, want[j]))
     assert O.status() == 0
 
 
