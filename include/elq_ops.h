@@ -156,6 +156,19 @@ elq_status elq_residual_norm(const elq_residual* r, void* stream);
  * device wait of a product ran out since the last read (its y is undefined). */
 elq_status elq_ops_status(void* stream);
 
+/* ---- test entry point --------------------------------------------------------------- */
+
+/* Failure detection of the products: elq_i8_matmul on the tensor cores with a wait
+ * that cannot end.  stall 1: the copies of the first tile stop one K step short; 2: no
+ * accumulator is given back, so that a CTA's (or a pair's) third tile waits for good
+ * (a product that gives none a third tile is not disturbed).  The wait runs out after
+ * budget_ns (1 ms .. 2 s); the kernel lets its copies and MMAs in flight end and
+ * returns, and elq_ops_status then says ELQ_ERR_TIMEOUT.  y is left undefined.
+ * ELQ_ERR_UNSUPPORTED where the product does not take the tensor cores. */
+elq_status elq_test_i8_matmul_timeout(const int8_t* x, int64_t ldx, const float* sx, int64_t T, const int8_t* w,
+                                      int64_t ldw, const float* sw, int32_t N, int32_t K, float* y, int64_t ldy,
+                                      int32_t stall, uint64_t budget_ns, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

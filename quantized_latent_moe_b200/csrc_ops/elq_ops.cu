@@ -241,6 +241,8 @@ struct Product {
     int y_type;
     int64_t ldy;
     int kind;
+    int stall = 0;              // a test's (MmaArgs)
+    uint64_t wait_ns = kOpsWaitNs;
 };
 
 template <int KIND, int R, int U>
@@ -320,6 +322,8 @@ bool mma_args(const Product& p, int cg, MmaArgs& a) {
     a.N = p.N;
     a.Kb = p.K * es;
     a.split = 1;
+    a.stall = p.stall;
+    a.wait_ns = p.wait_ns;
     a.idesc = mma_idesc(KIND, cg);
     a.sx = p.sx;
     a.sw = p.sw;
@@ -432,6 +436,18 @@ elq_status run_product(const Product& p, cudaStream_t s) {
                                                                                : launch_mma<KIND_F16>(p, s);
 }
 
+elq_status check_i8_matmul(const Product& p, int64_t T) {
+    if (T < 0 || p.N < 1 || p.K < 1 || p.ldx < p.K || p.ldw < p.K || p.ldy < p.N) return ELQ_ERR_INVALID_ARG;
+    if (!float_type(p.y_type) || p.K > kMaxK || T > kMaxSize || p.N > kMaxSize) return ELQ_ERR_UNSUPPORTED;
+    if (p.ldx % 16 || p.ldw % 16) return ELQ_ERR_ALIGNMENT;
+    if (T == 0) return ELQ_OK;
+    if (!p.x || !p.sx || !p.w || !p.sw || !p.y) return ELQ_ERR_INVALID_ARG;
+    if (!aligned(p.x, 16) || !aligned(p.w, 16) || !aligned(p.y, 16) || !aligned(p.sx, 4) || !aligned(p.sw, 4) ||
+        !aligned(p.bias, 4))
+        return ELQ_ERR_ALIGNMENT;
+    return ELQ_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -515,15 +531,21 @@ elq_status elq_combine_i8(const void* o, int32_t o_type, int64_t o_rows, int32_t
 elq_status elq_i8_matmul(const int8_t* x, int64_t ldx, const float* sx, int64_t T, const int8_t* w, int64_t ldw,
                          const float* sw, const float* bias, int32_t N, int32_t K, void* y, int32_t y_type, int64_t ldy,
                          void* stream) {
-    if (T < 0 || N < 1 || K < 1 || ldx < K || ldw < K || ldy < N) return ELQ_ERR_INVALID_ARG;
-    if (!float_type(y_type) || K > kMaxK || T > kMaxSize || N > kMaxSize) return ELQ_ERR_UNSUPPORTED;
-    if (ldx % 16 || ldw % 16) return ELQ_ERR_ALIGNMENT;
-    if (T == 0) return ELQ_OK;
-    if (!x || !sx || !w || !sw || !y) return ELQ_ERR_INVALID_ARG;
-    if (!aligned(x, 16) || !aligned(w, 16) || !aligned(y, 16) || !aligned(sx, 4) || !aligned(sw, 4) ||
-        !aligned(bias, 4))
-        return ELQ_ERR_ALIGNMENT;
     const Product p = {x, ldx, sx, (int)T, w, ldw, 0, sw, bias, 1, N, K, nullptr, y, y_type, ldy, KIND_I8};
+    const elq_status st = check_i8_matmul(p, T);
+    return st != ELQ_OK || T == 0 ? st : run_product(p, (cudaStream_t)stream);
+}
+
+elq_status elq_test_i8_matmul_timeout(const int8_t* x, int64_t ldx, const float* sx, int64_t T, const int8_t* w,
+                                      int64_t ldw, const float* sw, int32_t N, int32_t K, float* y, int64_t ldy,
+                                      int32_t stall, uint64_t budget_ns, void* stream) {
+    Product p = {x, ldx, sx, (int)T, w, ldw, 0, sw, nullptr, 1, N, K, nullptr, y, ELQ_F32, ldy, KIND_I8};
+    const elq_status st = check_i8_matmul(p, T);
+    if (st != ELQ_OK) return st;
+    if (stall < 1 || stall > 2 || budget_ns < 1000000ull || budget_ns > kOpsWaitNs) return ELQ_ERR_INVALID_ARG;
+    if (T == 0 || few_rows(p)) return ELQ_ERR_UNSUPPORTED;
+    p.stall = stall;
+    p.wait_ns = budget_ns;
     return run_product(p, (cudaStream_t)stream);
 }
 

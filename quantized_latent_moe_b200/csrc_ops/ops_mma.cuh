@@ -42,7 +42,7 @@ using elq::smem_addr;
 // elq_ops_status.
 __device__ int g_ops_err;
 
-constexpr uint64_t kOpsWaitNs = 2000000000ull;     // 2 s per bounded device wait
+constexpr uint64_t kOpsWaitNs = 2000000000ull;     // 2 s per bounded device wait (a test's are shorter)
 constexpr uint64_t kOpsDrainNs = 100000000ull;     // 0.1 s for what is in flight after one ran out
 constexpr int kMmaThreads = 384;
 constexpr int kMmaEpiWarps = 8;
@@ -63,6 +63,8 @@ struct alignas(64) MmaArgs {
     int bn;                     // most rows of a tile: a multiple of 32 a CTA, <= 256
     int stages;
     int split;                  // k_split: CTAs of a tile
+    int stall;                  // 0; a test's: 1 the first CTA's copies stop one K step short, 2 no accumulator is given back
+    uint64_t wait_ns;           // limit of a device wait
     uint32_t idesc;             // instruction descriptor without its N field
     const float* sx;
     const float* sw;
@@ -123,13 +125,21 @@ __device__ __forceinline__ void umma(uint32_t d, uint64_t ad, uint64_t bd, uint3
             "l"(ad), "l"(bd), "r"(idesc), "r"(acc)
             : "memory");
 }
-// An arrival on the barrier (in a pair: on both CTAs' barriers at this offset)
-// when all MMAs issued so far are done.
+// An arrival on this CTA's barrier when all MMAs issued so far are done.
 template <int CG>
-__device__ __forceinline__ void umma_commit(uint64_t* bar) {
+__device__ __forceinline__ void umma_commit_here(uint64_t* bar) {
     if constexpr (CG == 1)
         asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
                      : "memory");
+    else
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+                     : "memory");
+}
+// The same, in a pair on both CTAs' barriers at this offset.
+template <int CG>
+__device__ __forceinline__ void umma_commit(uint64_t* bar) {
+    if constexpr (CG == 1)
+        umma_commit_here<1>(bar);
     else
         asm volatile(
             "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
@@ -255,14 +265,14 @@ __device__ __forceinline__ bool bar_try(uint64_t* bar, uint32_t parity, uint32_t
 // clock is read only once a wait is long: reading it costs as much as a whole
 // step of the pipeline.
 template <bool CLUSTER = false>
-__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatile int* abort_v) {
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatile int* abort_v, uint64_t limit_ns) {
     for (int i = 0; i < 32; ++i)
         if (CLUSTER ? bar_try<true>(bar, parity, 0) : mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = global_timer_ns();
     for (uint32_t i = 0; i < (1u << 26); ++i) {
         if (bar_try<CLUSTER>(bar, parity, 20000u)) return true;
         if (*abort_v) return false;
-        if ((i & 15) == 15 && global_timer_ns() - t0 > kOpsWaitNs) break;
+        if ((i & 15) == 15 && global_timer_ns() - t0 > limit_ns) break;
     }
     *abort_v = 1;
     atomicExch(&g_ops_err, 1);
@@ -271,20 +281,41 @@ __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatil
 
 // The end of a cluster's work: no CTA leaves, and gives up its shared memory, while
 // another may still reach it.  Every CTA tells all `n` of them, itself included
-// (`bye` counts n), and waits, with a limit, for all to have told it.  By all threads.
-__device__ __forceinline__ void cluster_leave(uint64_t* bye, int n) {
+// (`bye` counts n), and waits, with a limit, for all to have told it: each of them may
+// have begun its last wait when this one's ran out, and may drain its ring after it.
+// By all threads.
+__device__ __forceinline__ void cluster_leave(uint64_t* bye, int n, uint64_t limit_ns) {
     __syncthreads();
     if ((int)threadIdx.x < n) bar_arrive_cluster(in_cta(bye, threadIdx.x));
     if (threadIdx.x == 0) {
         const uint64_t t0 = global_timer_ns();
         while (!bar_try<true>(bye, 0, 20000u)) {
-            if (global_timer_ns() - t0 > kOpsWaitNs + 10 * kOpsDrainNs) {
+            if (global_timer_ns() - t0 > 2 * limit_ns + (kMmaStagesMax + 2) * kOpsDrainNs) {
                 atomicExch(&g_ops_err, 2);
                 break;
             }
         }
     }
     __syncthreads();
+}
+
+// Waits, with a limit, for what is in flight: for a barrier's phase, and for the last
+// uses (up to `issued`) of a ring whose next use would be stage st in phase ph.
+__device__ __forceinline__ void bar_land(uint64_t* bar, uint32_t parity) {
+    for (int i = 0; i < 32; ++i)
+        if (mbar_try_wait(bar, parity)) return;
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait_hint(bar, parity, 20000u) && global_timer_ns() - t0 < kOpsDrainNs) {
+    }
+}
+__device__ __forceinline__ void ring_land(uint64_t* bars, int stages, long long issued, int st, uint32_t ph) {
+    for (int i = 0; i < stages && i < issued; ++i) {
+        if (--st < 0) {
+            st = stages - 1;
+            ph ^= 1;
+        }
+        bar_land(bars + st, ph);
+    }
 }
 
 // ---- units -----------------------------------------------------------------------
@@ -452,7 +483,11 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_mma(const __grid_constant__ 
                 const Unit x = unit_of<CG>(u, s_off, s_tile, a.E, ch_tiles);
                 const int boxes = (x.n / CG + kBoxRows - 1) / kBoxRows, row0 = x.row0 + rank * (x.n / CG);
                 for (int k = 0; k < steps; ++k) {
-                    if (!(ok = bar_wait(empty + st, ph ^ 1, abort_v))) break;
+                    if (a.stall == 1 && blockIdx.x < CG && k == steps - 1) {
+                        ok = false;
+                        break;
+                    }
+                    if (!(ok = bar_wait(empty + st, ph ^ 1, abort_v, a.wait_ns))) break;
                     const uint32_t p = tiles0 + st * stage_bytes, fb = CG == 1 ? smem_addr(full + st) : first_cta(full + st);
                     const int c = k * (KIND == KIND_I8 ? kStepBytes : kStepBytes / 2);
                     if (rank == 0) mbar_arrive_expect_tx(full + st, CG * (kABytes + boxes * kBoxBytes));
@@ -466,17 +501,9 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_mma(const __grid_constant__ 
                     }
                 }
             }
-            if (!ok) {
-                // let the copies in flight land before the CTA gives up its memory (a pair's second CTA cannot
-                // see them land: it gives them the whole time)
-                for (int i = 0; i < a.stages && i < issued; ++i) {
-                    const long long n = issued - 1 - i;
-                    const uint64_t t0 = global_timer_ns();
-                    while (!(rank == 0 && mbar_try_wait_hint(full + n % a.stages, (uint32_t)(n / a.stages) & 1, 20000u)) &&
-                           global_timer_ns() - t0 < kOpsDrainNs) {
-                    }
-                }
-            }
+            // No copy may be in flight when the CTA gives up its memory, whichever role's wait ran out: the
+            // last use of every stage is waited for (a pair's second CTA sees only that the MMAs read it).
+            ring_land(rank == 0 ? full : empty, a.stages, issued, st, ph);
         }
     } else if (warp == 1) {
         if (rank == 0 && elect_one()) {
@@ -486,11 +513,11 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_mma(const __grid_constant__ 
             for (int u = u0; ok && u < units; u += du, ++it) {
                 const Unit x = unit_of<CG>(u, s_off, s_tile, a.E, ch_tiles);
                 const int acc = it & 1;
-                if (!(ok = bar_wait<CG == 2>(tempty + acc, ((it >> 1) & 1) ^ 1, abort_v))) break;
+                if (!(ok = bar_wait<CG == 2>(tempty + acc, ((it >> 1) & 1) ^ 1, abort_v, a.wait_ns))) break;
                 tc_after();
                 const uint32_t idesc = a.idesc | ((uint32_t)(x.n >> 3) << 17), d = tmem + acc * 256;
                 for (int k = 0; k < steps; ++k) {
-                    if (!(ok = bar_wait(full + st, ph, abort_v))) break;
+                    if (!(ok = bar_wait(full + st, ph, abort_v, a.wait_ns))) break;
                     tc_after();
                     const uint32_t p = tiles0 + st * stage_bytes;
                     const uint64_t ad = sw128_desc(p), bd = sw128_desc(p + kABytes);
@@ -509,12 +536,8 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_mma(const __grid_constant__ 
                 }
                 if (ok) umma_commit<CG>(tfull + acc);
             }
-            if (!ok) {
-                umma_commit<CG>(drain);
-                const uint64_t t0 = global_timer_ns();
-                while (!mbar_try_wait_hint(drain, 0, 20000u) && global_timer_ns() - t0 < kOpsDrainNs) {
-                }
-            }
+            umma_commit_here<CG>(drain);    // nor an MMA
+            bar_land(drain, 0);
         }
     } else if (CG == 2 && warp == 3) {
         // A pair's accumulators go back to the first CTA, which issues the MMAs, by a release at cluster
@@ -524,7 +547,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_mma(const __grid_constant__ 
         if (elect_one()) {
             int it = 0;
             for (int u = u0; u < units; u += du, ++it) {
-                if (!bar_wait(tdone + (it & 1), (it >> 1) & 1, abort_v)) break;
+                if (!bar_wait(tdone + (it & 1), (it >> 1) & 1, abort_v, a.wait_ns)) break;
                 bar_arrive_cluster(first_cta(tempty + (it & 1)));
             }
         }
@@ -540,13 +563,13 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_mma(const __grid_constant__ 
                 sw = __ldg(a.sw + (int64_t)x.e * a.N + n);
                 if (a.bias) bias = __ldg(a.bias + n);
             }
-            if (!__all_sync(0xffffffffu, bar_wait(tfull + acc, (it >> 1) & 1, abort_v))) break;
+            if (!__all_sync(0xffffffffu, bar_wait(tfull + acc, (it >> 1) & 1, abort_v, a.wait_ns))) break;
             tc_after();
             // The accumulator goes back as soon as this warp's last values of it are in registers.
             auto give_back = [&] {
                 tc_before();
                 __syncwarp();
-                if (lane == 0) bar_arrive((CG == 1 ? tempty : tdone) + acc);
+                if (lane == 0 && a.stall != 2) bar_arrive((CG == 1 ? tempty : tdone) + acc);
             };
             if (half * 32 >= x.rows) give_back();
             for (int c = half * 32; c < x.rows; c += 64) {
@@ -575,7 +598,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_mma(const __grid_constant__ 
     __syncwarp();
     tc_before();
     if (CG == 1) __syncthreads();
-    else cluster_leave(bye, CG);
+    else cluster_leave(bye, CG, a.wait_ns);
     tc_after();
     if (warp == 2) tmem_free<CG>(tmem, 512);
 }
@@ -631,9 +654,9 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_split(const __grid_constant_
         if (elect_one()) {
             int st = 0, issued = 0;
             uint32_t ph = 0;
-            bool ok = true;
             for (int k = k0; k < k1; ++k) {
-                if (!(ok = bar_wait(empty + st, ph ^ 1, abort_v))) break;
+                if (a.stall == 1 && blockIdx.x == 0 && k == k1 - 1) break;
+                if (!bar_wait(empty + st, ph ^ 1, abort_v, a.wait_ns)) break;
                 const uint32_t p = tiles0 + st * stage_bytes, fb = smem_addr(full + st);
                 const int c = k * (KIND == KIND_I8 ? kStepBytes : kStepBytes / 2);
                 mbar_arrive_expect_tx(full + st, kABytes + boxes * kBoxBytes);
@@ -645,13 +668,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_split(const __grid_constant_
                     ph ^= 1;
                 }
             }
-            for (int i = 0; !ok && i < a.stages && i < issued; ++i) {       // as in k_mma
-                const int m = issued - 1 - i;
-                const uint64_t t0 = global_timer_ns();
-                while (!mbar_try_wait_hint(full + m % a.stages, (uint32_t)(m / a.stages) & 1, 20000u) &&
-                       global_timer_ns() - t0 < kOpsDrainNs) {
-                }
-            }
+            ring_land(full, a.stages, issued, st, ph);      // as in k_mma
         }
     } else if (warp == 1) {
         if (elect_one()) {
@@ -659,7 +676,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_split(const __grid_constant_
             uint32_t ph = 0;
             const uint32_t idesc = a.idesc | ((uint32_t)(n >> 3) << 17);
             for (int k = k0; k < k1; ++k) {
-                if (!bar_wait(full + st, ph, abort_v)) break;
+                if (!bar_wait(full + st, ph, abort_v, a.wait_ns)) break;
                 tc_after();
                 const uint32_t p = tiles0 + st * stage_bytes;
                 const uint64_t ad = sw128_desc(p), bd = sw128_desc(p + kABytes);
@@ -677,12 +694,13 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_split(const __grid_constant_
                 }
             }
             umma_commit<1>(tfull);      // also after a wait that ran out: nothing may be in flight at the end
+            bar_land(tfull, 0);
         }
     }
     __syncwarp();
     // Every warp waits for the MMAs (the ring is free then), eight of them move
     // the accumulators: word (row, channel) at part[row * 128 + channel].
-    const bool done = __all_sync(0xffffffffu, bar_wait(tfull, 0, abort_v));
+    const bool done = __all_sync(0xffffffffu, bar_wait(tfull, 0, abort_v, a.wait_ns));
     __syncthreads();                    // and no warp reads a barrier in the ring's way any more
     tc_after();
     uint32_t* part = reinterpret_cast<uint32_t*>(smem + (tiles0 - smem_addr(smem)));
@@ -772,7 +790,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_split(const __grid_constant_
                 if (ch + j < a.N) store1(a.y, a.y_type, at + j, v[j]);
         }
     }
-    cluster_leave(bye, S);
+    cluster_leave(bye, S, a.wait_ns);
 }
 
 }  // namespace elqops

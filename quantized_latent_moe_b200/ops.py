@@ -44,6 +44,7 @@ SIGNATURES = {
     "elq_rms_norm": (I32, [V, I32, I64, I32, I64, V, F, V, I32, I64, V, V]),
     "elq_residual_norm": (I32, [ctypes.POINTER(ResidualC), V]),
     "elq_ops_status": (I32, [V]),
+    "elq_test_i8_matmul_timeout": (I32, [V, I64, V, I64, V, I64, V, I32, I32, V, I64, I32, ctypes.c_uint64, V]),
 }
 
 _L = None

@@ -736,6 +736,27 @@ def test_pairs_on_two_streams(O):
     assert O.status() == 0
 
 
+def pointers(O, x, w, y):
+    return (x.q.data_ptr(), x.q.stride(0), x.scale.data_ptr(), x.q.shape[0], w.q.data_ptr(), w.q.stride(0), w.scale.data_ptr(),
+            w.q.shape[0], x.q.shape[1], y.data_ptr(), y.stride(0))
+
+
+@pytest.mark.parametrize("T,N,K,stall", [(16, 300, 2048, 1), (2048, 1792, 1024, 1), (2500, 2304, 1024, 1), (2500, 2304, 64, 1),
+                                         (8192, 4096, 1024, 2)])
+def test_wait_that_runs_out(O, T, N, K, stall):
+    """A product whose device wait cannot end (split over K, single CTAs, pairs): it comes back within its limits, the
+    error word says so once, and the next product is right."""
+    import ctypes
+    g = rng(T + N)
+    x, w = O.quantize_i8(randn(g, T, K)), O.quantize_i8(randn(g, N, K))
+    want, y = O.i8_matmul(x, w), torch.empty(T, N, device="cuda")
+    assert O.status() == 0
+    stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    assert O.lib().elq_test_i8_matmul_timeout(*pointers(O, x, w, y), stall, 20_000_000, stream) == 0
+    assert O.status() == -6 and O.status() == 0
+    assert torch.equal(O.i8_matmul(x, w), want) and O.status() == 0
+
+
 def test_stream_argument(O):
     st = torch.cuda.Stream()
     g = rng(8)

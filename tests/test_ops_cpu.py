@@ -84,6 +84,16 @@ def test_matmul_refusals(L, over, status):
     assert L.elq_i8_matmul(*_args(MATMUL, over)) == status
 
 
+TIMEOUT = dict(x=P, ldx=64, sx=P, T=16, w=P, ldw=64, sw=P, N=32, K=64, y=P, ldy=32, stall=1, budget=1 << 24, stream=None)
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(stall=0), -1), (dict(stall=3), -1), (dict(budget=999_999), -1), (dict(budget=2_000_000_001), -1), (dict(T=4), -2),
+    (dict(T=0), -2), (dict(x=None), -1), (dict(ldy=31), -1), (dict(ldx=72), -3), (dict(T=-1), -1)])
+def test_timeout_refusals(L, over, status):
+    assert L.elq_test_i8_matmul_timeout(*_args(TIMEOUT, over)) == status
+
+
 GROUPED = dict(x=P, x_type=24, ldx=64, sx=P, M=4, w=P, ldw=64, w_stride=64 * 32, sw=P, E=8, N=32, K=64, offsets=P, y=P,
                y_type=0, ldy=32, stream=None)
 G16 = dict(x_type=30, sx=None, sw=None)
