@@ -151,9 +151,10 @@ elq_status elq_residual_norm(const elq_residual* r, void* stream);
 
 /* ---- status ---------------------------------------------------------------------- */
 
-/* Blocking: synchronises `stream`, reads the current device's error word of the
- * calls in this header and clears it; ELQ_OK, or ELQ_ERR_TIMEOUT if a bounded
- * device wait of a product ran out since the last read (its y is undefined). */
+/* Blocking: synchronises `stream` (and no other), reads the current device's error
+ * word of the calls in this header and clears it, in one step; ELQ_OK, or
+ * ELQ_ERR_TIMEOUT if a bounded device wait of a product ran out since the last read
+ * (its y is undefined). */
 elq_status elq_ops_status(void* stream);
 
 /* ---- test entry point --------------------------------------------------------------- */

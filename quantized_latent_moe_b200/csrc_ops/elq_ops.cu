@@ -655,13 +655,17 @@ elq_status elq_residual_norm(const elq_residual* r, void* stream) {
 }
 
 elq_status elq_ops_status(void* stream) {
-    if (cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess) return ELQ_ERR_CUDA;
+    static std::mutex one;      // g_ops_said is one caller's at a time
+    cudaStream_t s = (cudaStream_t)stream;
+    if (cudaStreamSynchronize(s) != cudaSuccess) return ELQ_ERR_CUDA;
     int err = 0;
-    if (cudaMemcpyFromSymbol(&err, g_ops_err, sizeof(err)) != cudaSuccess) return ELQ_ERR_CUDA;
-    if (!err) return ELQ_OK;
-    const int zero = 0;
-    if (cudaMemcpyToSymbol(g_ops_err, &zero, sizeof(zero)) != cudaSuccess) return ELQ_ERR_CUDA;
-    return ELQ_ERR_TIMEOUT;
+    std::lock_guard<std::mutex> lock(one);
+    k_status<<<1, 1, 0, s>>>();
+    if (cudaGetLastError() != cudaSuccess ||
+        cudaMemcpyFromSymbolAsync(&err, g_ops_said, sizeof(err), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+        cudaStreamSynchronize(s) != cudaSuccess)
+        return ELQ_ERR_CUDA;
+    return err ? ELQ_ERR_TIMEOUT : ELQ_OK;
 }
 
 }  // extern "C"

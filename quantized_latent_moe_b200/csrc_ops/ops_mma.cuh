@@ -38,9 +38,12 @@ using elq::mbar_try_wait;
 using elq::mbar_try_wait_hint;
 using elq::smem_addr;
 
-// Set by a product whose bounded wait ran out; read and cleared by
-// elq_ops_status.
+// Set by a product whose bounded wait ran out; read and cleared in one step by
+// k_status, so that no other stream's is lost between the two.
 __device__ int g_ops_err;
+__device__ int g_ops_said;      // what k_status read
+
+inline __global__ void k_status() { g_ops_said = atomicExch(&g_ops_err, 0); }
 
 constexpr uint64_t kOpsWaitNs = 2000000000ull;     // 2 s per bounded device wait (a test's are shorter)
 constexpr uint64_t kOpsDrainNs = 100000000ull;     // 0.1 s for what is in flight after one ran out

@@ -757,6 +757,26 @@ def test_wait_that_runs_out(O, T, N, K, stall):
     assert torch.equal(O.i8_matmul(x, w), want) and O.status() == 0
 
 
+def test_status_waits_for_its_own_stream_only(O):
+    """While the default stream is busy, another stream's status comes back; what the default stream's product sets
+    after that is still reported."""
+    import ctypes
+    side, (x, w) = torch.cuda.Stream(), (O.quantize_i8(torch.randn(16, 512, device="cuda")), O.quantize_i8(torch.randn(300, 512, device="cuda")))
+    y, done = O.i8_matmul(x, w), torch.cuda.Event()
+    assert O.status(stream=side) == 0       # the first use of a kernel loads it, which may wait for the device
+    torch.cuda._sleep(1_000_000_000)
+    stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    assert O.lib().elq_test_i8_matmul_timeout(*pointers(O, x, w, y), 1, 5_000_000, stream) == 0
+    done.record()
+    seen = O.status(stream=side)
+    assert seen == 0 and not done.query()
+    reports = 0
+    while not done.query():
+        reports += O.status(stream=side) == -6
+    reports += O.status() == -6
+    assert reports == 1 and O.status() == 0
+
+
 def test_stream_argument(O):
     st = torch.cuda.Stream()
     g = rng(8)
