@@ -11,7 +11,8 @@ contiguous, or whose rows are not whole multiples of 16 bytes apart where the ca
 needs it, is refused.  There is no fallback; a missing library raises.
 
 ``stream`` is a ``torch.cuda.Stream`` (the current one by default); outputs are
-allocated on it.  Calls run on the device of their tensors, whatever the current
+allocated on it, and inputs recorded on it, so that their memory is not given out
+again while it is read (that they are ready is the caller's to see to).  Calls run on the device of their tensors, whatever the current
 device is.  ``lib()`` gives the C entries themselves, for callers that hold addresses.
 """
 from __future__ import annotations
@@ -127,7 +128,12 @@ def _on(stream, x, call, *args, **kw):
     if stream.device != t.device:
         raise ElqError(-1, "stream: of another device")
     with torch.cuda.stream(stream):
-        return call(x, *args, **kw)
+        out = call(x, *args, **kw)
+    for a in (x, *args, *kw.values()):
+        for t in (a._q, a._scale, a._buf) if isinstance(a, I8Rows) else (a,):
+            if isinstance(t, torch.Tensor):
+                t.record_stream(stream)
+    return out
 
 
 # ---- rows to codes --------------------------------------------------------------

@@ -789,6 +789,38 @@ def test_stream_argument(O):
     assert torch.equal(got, want)
 
 
+def test_stream_argument_keeps_inputs(O):
+    """Inputs dropped right after a call on another stream keep their memory until that stream has read them."""
+    side, g, n = torch.cuda.Stream(), rng(9), 1 << 22
+    w = O.quantize_i8(randn(g, 64, 1024))
+    calls = [lambda t: O.quantize_i8(t, stream=side), lambda t: O.rms_norm(t, stream=side),
+             lambda t: O.residual_norm(t, t, next_dtype=torch.int8, stream=side)]
+    make = lambda: torch.ones(n // 1024, 1024, device="cuda")
+    for call in calls:
+        call(make())                                    # kernels loaded, streams known to the allocator
+    O.i8_matmul(O.quantize_i8(make()), w, stream=side)
+    torch.cuda.synchronize()
+    for call in calls:
+        t = make()
+        at = t.data_ptr()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(200_000_000)
+        call(t)
+        del t
+        assert make().data_ptr() != at
+        torch.cuda.synchronize()
+    xq = O.quantize_i8(make())
+    at = xq.q.data_ptr()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)
+    O.i8_matmul(xq, w, stream=side)
+    del xq
+    assert O.quantize_i8(make()).q.data_ptr() != at
+    torch.cuda.synchronize()
+
+
 def test_binding_refusals(O):
     from quantized_latent_moe_b200.elq import ElqError
     g = rng(1)
