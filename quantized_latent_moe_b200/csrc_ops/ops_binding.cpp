@@ -193,6 +193,8 @@ at::Tensor output(PyObject* out, int64_t rows, int64_t cols, int type, int dev, 
     const at::Tensor& t = tensor(out, what);
     m = matrix(t, what, FLOATS, dev);
     check(m.type == type && m.rows == rows && m.cols == cols, what);
+    // what autograd has saved of it is no longer what it was
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
     return t;
 }
 

@@ -7,8 +7,13 @@ csrc_ops/ops_binding.cpp), because the host's time bounds the small calls.  Ever
 function checks what the C entry cannot see (devices, dtypes, shapes, strides),
 allocates its outputs, and makes one C call, raising ``elq.ElqError`` where that
 refuses.  Nothing is copied or cast on the way: a tensor whose rows are not
-contiguous, or whose rows are not whole multiples of 16 bytes apart where the call
-needs it, is refused.  There is no fallback; a missing library raises.
+contiguous, whose first row is not on a 16-byte boundary (h[1:] of odd width, say), or
+whose rows are not whole multiples of 16 bytes apart where the call needs it, is
+refused.  There is no fallback; a missing library raises.
+
+The calls infer only: outputs have no autograd graph, whatever their inputs require.
+An ``out`` counts as written in place (its version goes up), so that a backward pass
+that had saved it says so instead of using it.
 
 ``stream`` is a ``torch.cuda.Stream`` (the current one by default); outputs are
 allocated on it, and inputs recorded on it, so that their memory is not given out

@@ -821,6 +821,25 @@ def test_stream_argument_keeps_inputs(O):
     torch.cuda.synchronize()
 
 
+def test_out_counts_as_written_in_place(O):
+    """A backward pass that saved what a call then writes raises, and does not use the new values."""
+    h, y = torch.randn(4, 64, device="cuda"), torch.randn(4, 64, device="cuda")
+    w = torch.ones(4, 64, device="cuda", requires_grad=True)
+    (xq, m), off = (O.quantize_i8(h), O.quantize_i8(torch.randn(64, 64, device="cuda"))), offsets_of([4])
+    for write in (lambda: O.rms_norm(h, out=h), lambda: O.residual_norm(h, y, out=h), lambda: O.i8_matmul(xq, m, out=h),
+                  lambda: O.grouped_matmul(xq, O.I8Rows(m.q.unsqueeze(0), m.scale.unsqueeze(0)), off, out=h)):
+        loss = (w * h).sum()
+        before = h._version
+        write()
+        assert h._version > before
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+    with torch.inference_mode():
+        t = torch.randn(4, 64, device="cuda")
+        O.rms_norm(t, out=t)
+    O.rms_norm(t, out=t)
+
+
 def test_binding_refusals(O):
     from quantized_latent_moe_b200.elq import ElqError
     g = rng(1)
