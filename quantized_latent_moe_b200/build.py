@@ -3,6 +3,7 @@ sm_100a, and _ops.so, the compiled Python binding of the latter, with the host c
 from __future__ import annotations
 
 import glob
+import importlib.metadata
 import os
 import subprocess
 import sys
@@ -15,6 +16,7 @@ OBJ = os.path.join(HERE, "_build")          # one object per source, rebuilt whe
 LIB = os.path.join(HERE, "libelq.so")
 BINDING = os.path.join(HERE, "_ops.so")
 BINDING_SRC = os.path.join(CSRC[1], "ops_binding.cpp")
+BINDING_FOR = os.path.join(OBJ, "_ops.for")     # what _ops.so was built against
 CXX = os.environ.get("CXX", "g++")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
@@ -57,6 +59,22 @@ def _stale(target, sources):
     return not os.path.exists(target) or os.path.getmtime(target) < max(os.path.getmtime(p) for p in sources)
 
 
+def binding_abi():
+    """_ops.so holds for one Python and one torch; another of either needs another build."""
+    return "%s torch %s" % (sys.implementation.cache_tag, importlib.metadata.version("torch"))
+
+
+def _binding_stale():
+    if _stale(BINDING, [BINDING_SRC, os.path.join(ROOT, "include", "elq.h"), os.path.join(ROOT, "include", "elq_ops.h"),
+                        __file__]):
+        return True
+    try:
+        with open(BINDING_FOR) as f:
+            return f.read() != binding_abi()
+    except OSError:
+        return True
+
+
 def _binding_cmd(out):
     import torch
     root = os.path.dirname(torch.__file__)
@@ -86,11 +104,14 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         tmp = LIB + ".tmp%d" % os.getpid()
         out += _run([[NVCC, *FLAGS, "-shared", "-o", tmp, *objs]])
         os.replace(tmp, LIB)
-    if force or _stale(BINDING, [BINDING_SRC, os.path.join(ROOT, "include", "elq.h"),
-                                 os.path.join(ROOT, "include", "elq_ops.h"), __file__]):
+    if force or _binding_stale():
+        os.makedirs(OBJ, exist_ok=True)
         tmp = BINDING + ".tmp%d" % os.getpid()
         out += _run([_binding_cmd(tmp)])
         os.replace(tmp, BINDING)
+        with open(BINDING_FOR + ".tmp%d" % os.getpid(), "w") as f:
+            f.write(binding_abi())
+        os.replace(f.name, BINDING_FOR)
     if verbose:
         sys.stderr.write(out)
     return LIB

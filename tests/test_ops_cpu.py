@@ -3,6 +3,7 @@ symbol is exported and bound, and bad arguments are refused on the host before
 any launch (every case here fails validation or has no rows, so nothing is ever
 enqueued)."""
 import ctypes
+import importlib.metadata
 import os
 import re
 
@@ -156,6 +157,31 @@ def test_binding_refuses_host_tensors_and_shapes(L):
                  lambda: ops.quantize_i8(x[0]), lambda: ops.i8_matmul(x, rows), lambda: ops.rms_norm(x.double())):
         with pytest.raises(elq.ElqError):
             call()
+
+
+def test_binding_is_rebuilt_for_another_torch_or_python(L, monkeypatch, tmp_path):
+    """The compiled binding holds for the torch and Python that it was built against, and for no other."""
+    ran = []
+
+    def run(cmds):
+        ran.extend(cmds)
+        open(cmds[0][cmds[0].index("-o") + 1], "w").close()
+        return ""
+
+    made = tmp_path / "_ops.so"
+    made.write_text("")
+    monkeypatch.setattr(build, "BINDING", str(made))
+    monkeypatch.setattr(build, "BINDING_FOR", str(tmp_path / "_ops.for"), raising=False)
+    monkeypatch.setattr(build, "_run", run)
+    build.build()
+    first = len(ran)
+    build.build()
+    assert len(ran) == first                            # up to date
+    monkeypatch.setattr(importlib.metadata, "version", lambda name: "0.0.0")
+    build.build()
+    assert len(ran) == first + 1                        # another torch
+    build.build()
+    assert len(ran) == first + 1
 
 
 def test_dequantize():
