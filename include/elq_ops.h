@@ -117,7 +117,7 @@ elq_status elq_grouped_matmul(const void* x, int32_t x_type, int64_t ldx, const 
  * NULL (ones); eps > 0.  n: device [T][cols], n_type F32, BF16, F16, or I8: the
  * fp32 norm handed straight to the row quantiser (ldn a multiple of 16, scale:
  * device fp32 [T]; else scale is NULL).  n may be x itself where their types
- * and leading dimensions agree.  |x| below about 1e18 (the squares are fp32). */
+ * and leading dimensions agree.  |x| up to 1e36. */
 elq_status elq_rms_norm(const void* x, int32_t x_type, int64_t T, int32_t cols, int64_t ldx, const float* weight,
                         float eps, void* n, int32_t n_type, int64_t ldn, float* scale, void* stream);
 
@@ -127,7 +127,7 @@ elq_status elq_rms_norm(const void* x, int32_t x_type, int64_t T, int32_t cols, 
  *   h' = res_scale * h[t] + gate * v
  *   n  = h' / sqrt(mean(h'^2) + eps) * next_weight        (of the unrounded h')
  * All of it fp32 (where all rows share the gate it meets post_weight first), h'
- * and n each rounded once. */
+ * and n each rounded once; |y| and |h'| up to 1e36. */
 typedef struct {
     int64_t T;
     int32_t cols;

@@ -422,6 +422,34 @@ __device__ __forceinline__ float rstd_of(float ss, float inv_cols, float eps) {
     return rsqrtf(__fmaf_rn(ss, inv_cols, eps));
 }
 
+// A row's factor from its threads' sums of squares.  Where their sum passes fp32 (values from
+// 1.8e19 / sqrt(cols) on) it is taken again after `down`, which has multiplied the values by 2^-80;
+// the factor is then that of those.  The sum is the same for all threads of the row, and so is the way.
+constexpr float kDown = 8.27180613e-25f;        // 2^-80
+
+// COMPACT: one copy of the code for both, a loop, which is what kernels short of registers want
+// (777 x 1283 fp16 residual norm: 8.6 us, 11.2 without); the others do without the loop (2048 x 4096
+// bf16: 18.1 us, 18.3 with).
+template <bool COMPACT, typename Reduce, typename Sum, typename Down>
+__device__ __forceinline__ float row_rstd(Reduce& rr, float inv_cols, float eps, Sum sum, Down down) {
+    const float inf = __uint_as_float(0x7f800000u), low = __fmul_rn(__fmul_rn(eps, kDown), kDown);
+    if constexpr (COMPACT) {
+        float e = eps;
+#pragma unroll 1
+        while (true) {
+            const float ss = rr.sum(sum());
+            if (ss != inf || e != eps) return rstd_of(ss, inv_cols, e);
+            down();
+            e = low;
+        }
+    } else {
+        const float ss = rr.sum(sum());
+        if (ss != inf) return rstd_of(ss, inv_cols, eps);
+        down();
+        return rstd_of(rr.sum(sum()), inv_cols, low);
+    }
+}
+
 // silu(g) * u in the formula's own steps: expf (CUDA's, within one ulp, 2^-23 of its value), the
 // sum, the quotient and the product.  The quotient is Markstein's: q = g / d by an approximate
 // reciprocal (2^-23), then its remainder added back once, which leaves 2^-45 beside the one
@@ -491,6 +519,21 @@ __device__ __forceinline__ void source8(const RowArgs& a, int64_t row, int64_t s
     } else {
         get8<VEC>(a.x, a.x_type, row * a.ldx, ci, a.cols, v);
     }
+}
+
+template <int NV>
+__device__ __forceinline__ float sumsq(const float (&v)[NV][8]) {
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) s = sumsq8(s, v[i]);
+    return s;
+}
+template <int NV>
+__device__ __forceinline__ void times(float (&v)[NV][8], float f) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] = __fmul_rn(v[i][j], f);
 }
 
 template <bool VEC>
@@ -585,10 +628,7 @@ __global__ void __maxnreg__(VPT == 1 && OP != ROW_COMBINE ? 56 : 128) k_rows(con
                 }
             }
             if constexpr (OP == ROW_RESIDUAL) {
-                float ss = 0.0f;
-#pragma unroll
-                for (int i = 0; i < NV; ++i) ss = sumsq8(ss, v[i]);
-                const float rstd = rstd_of(rr.sum(ss), a.inv_cols, a.eps);
+                const float rstd = row_rstd<true>(rr, a.inv_cols, a.eps, [&] { return sumsq(v); }, [&] { times(v, kDown); });
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
                     if (i >= nch) continue;
@@ -602,10 +642,7 @@ __global__ void __maxnreg__(VPT == 1 && OP != ROW_COMBINE ? 56 : 128) k_rows(con
                 if (!a.n) continue;
             }
             if constexpr (NORM) {
-                float ss = 0.0f;
-#pragma unroll
-                for (int i = 0; i < NV; ++i) ss = sumsq8(ss, v[i]);
-                const float rstd = rstd_of(rr.sum(ss), a.inv_cols, a.eps);
+                const float rstd = row_rstd<true>(rr, a.inv_cols, a.eps, [&] { return sumsq(v); }, [&] { times(v, kDown); });
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
                     if (i >= nch) continue;
@@ -644,22 +681,24 @@ __global__ void __maxnreg__(VPT == 1 && OP != ROW_COMBINE ? 56 : 128) k_rows(con
                 weight8<VEC>(OP == ROW_RMS ? a.w : a.w_next, i, a.cols, w);
                 norm8(w, rstd2, t);
             };
-            if constexpr (OP == ROW_RESIDUAL) {
-                float ss = 0.0f;
-                for (int i = 0; i < nch; ++i) {
-                    source8<OP, VEC, B>(a, row, src, i, t);
-                    ss = sumsq8(ss, t);
-                }
-                rstd = rstd_of(rr.sum(ss), a.inv_cols, a.eps);
-            }
-            if (OP == ROW_RMS || (OP == ROW_RESIDUAL && a.n)) {
-                float ss = 0.0f;
-                for (int i = 0; i < nch; ++i) {
-                    value(i);
-                    ss = sumsq8(ss, t);
-                }
-                rstd2 = rstd_of(rr.sum(ss), a.inv_cols, a.eps);
-            }
+            // the factor of the values that `get` puts into t, which are read again each time
+            auto factor = [&](auto&& get) {
+                float f = 1.0f;
+                auto sum = [&] {
+                    float ss = 0.0f;
+                    for (int i = 0; i < nch; ++i) {
+                        get(i);
+                        times(v, f);
+                        ss = sumsq8(ss, t);
+                    }
+                    return ss;
+                };
+                const float r = row_rstd<true>(rr, a.inv_cols, a.eps, sum, [&] { f = kDown; });
+                return __fmul_rn(r, f);
+            };
+            if constexpr (OP == ROW_RESIDUAL)
+                rstd = factor([&](int i) { source8<OP, VEC, B>(a, row, src, i, t); });
+            if (OP == ROW_RMS || (OP == ROW_RESIDUAL && a.n)) rstd2 = factor(value);
             CodeScale cs = code_scale(0);
             if (codes && a.n) {
                 float m = 0.0f;
@@ -786,6 +825,13 @@ __device__ __forceinline__ float sumsq(const f32x2 (&v)[VPT][4]) {
     const float2 h = halves(s);
     return __fadd_rn(h.x, h.y);
 }
+template <int VPT>
+__device__ __forceinline__ void times(f32x2 (&v)[VPT][4], float f) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[i][j] = mul2(v[i][j], pair(f, f));
+}
 
 // A CTA works on blockDim.y rows at a time, blockDim.x threads each, which share
 // the weights in shared memory.  D stages: the rows in shared memory per row
@@ -884,7 +930,7 @@ __global__ void __launch_bounds__(VPT == 1 ? kRowThreads : kPipeThreads4, 2) k_p
             }
         }
         if constexpr (OP == ROW_RESIDUAL) {
-            const float rstd = rstd_of(rr.sum(sumsq(v)), a.inv_cols, a.eps);
+            const float rstd = row_rstd<false>(rr, a.inv_cols, a.eps, [&] { return sumsq(v); }, [&] { times(v, kDown); });
             const float g0 = a.gate && a.gate_cols == 1 ? a.gate[(row / a.gate_rows) * a.gate_ld] : 1.0f;
             uint8_t* o = op + row * bo;
 #pragma unroll
@@ -914,7 +960,7 @@ __global__ void __launch_bounds__(VPT == 1 ? kRowThreads : kPipeThreads4, 2) k_p
             if (!a.n) continue;
         }
         if constexpr (OP == ROW_RMS || OP == ROW_RESIDUAL) {
-            const float rstd = rstd_of(rr.sum(sumsq(v)), a.inv_cols, a.eps);
+            const float rstd = row_rstd<false>(rr, a.inv_cols, a.eps, [&] { return sumsq(v); }, [&] { times(v, kDown); });
             uint8_t* o = np + row * bn;
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {

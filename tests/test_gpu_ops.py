@@ -270,6 +270,29 @@ def test_rms_norm_in_place_zero_and_out(O):
         assert torch.equal(v, ref)
 
 
+@pytest.mark.parametrize("x", ["f32", "bf16"])
+@pytest.mark.parametrize("T,C,ld", [(1, 4096, None), (700, 4096, None), (5, 1283, 1289), (2, 12000, None), (2, 20000, None), (400, 64, None)])
+def test_norms_of_large_values(O, x, T, C, ld):
+    """Rows whose sum of squares passes fp32, up to 1e36, beside ordinary ones, and rows with an infinity or a NaN."""
+    g = rng(C)
+    v = randn(g, T, C, ld=ld)
+    v *= torch.tensor([5e17, 1.0, 1e25, 1e35, 1e-3], device="cuda").repeat(T)[:T, None]
+    v = torch.nn.functional.pad(v, (0, 7))[:, :C].to(DT[x])
+    w = randn(g, C)
+    ref = rms64(v, w, 1e-5)
+    check(O.rms_norm(v, w, eps=1e-5, out_dtype=torch.float32), ref, NORM * ref.abs(), torch.float32)
+    check_codes(O.rms_norm_i8(v, w, eps=1e-5), ref, NORM * ref.abs())
+    ones = torch.ones(T, C, device="cuda")
+    h, n = O.residual_norm(ones, v, w, next_dtype=torch.float32)
+    ref = rms64(v, w, 1e-6)
+    check(h, ref + 1, NORM * ref.abs() + 2 * U32 * (ref.abs() + 1), torch.float32)
+    # h' large: y is zero, the gate irrelevant, n the norm of h alone
+    h, n = O.residual_norm(v.float(), torch.zeros(T, C, device="cuda"), next_weight=w, next_dtype=torch.float32)
+    check(n, ref, NORM * ref.abs(), torch.float32)
+    v[0, C // 2] = float("inf")
+    assert not bool(O.rms_norm(v)[0].isfinite().all()) and bool(O.rms_norm_i8(v).scale[0].isnan())
+
+
 @pytest.mark.parametrize("h,y,n", [("f32", "f32", "bf16"), ("bf16", "bf16", "bf16"), ("f16", "f32", "i8"), ("f32", "bf16", "i8"),
                                    ("bf16", "f16", "f32"), ("f16", "f16", None)])
 @pytest.mark.parametrize("T,C,pad,gate", [(1, 4096, 0, "channel"), (1, 1, 0, "token"), (6, 9, 2, "none"), (777, 1283, 6, "token"),
