@@ -369,8 +369,8 @@ elq_status launch_mma(const Product& p, cudaStream_t s) {
 // rows takes 150 + 0.4 bn, the exchange 400 + 17 a row.  (4096 -> 1792: 16 rows
 // 6.6 us against 10.4 unsplit, 256 rows 9.0 against 12.5; from about 1000 rows on
 // the tiles fill the SMs.)
-int split_plan(const Product& p, int es, int* bn) {
-    const int sms = device_sms(), steps = (int)(((int64_t)p.K * es + kStepBytes - 1) / kStepBytes);
+int split_plan(const Product& p, int* bn) {
+    const int sms = device_sms(), steps = (p.K + kStepBytes - 1) / kStepBytes;
     const int64_t ch_tiles = ((int64_t)p.N + kTileCh - 1) / kTileCh;
     const int bn1 = row_tile(p, sms, 1);
     if ((p.M + bn1 - 1) / bn1 * ch_tiles > sms) return 1;
@@ -390,18 +390,17 @@ int split_plan(const Product& p, int es, int* bn) {
     return best;
 }
 
-template <int KIND>
 elq_status launch_split(const Product& p, int split, int bn, cudaStream_t s) {
     static bool optin[kMaxDevices];
     MmaArgs a;
-    if (!mma_args<KIND>(p, 1, a) || !mma_optin(k_split<KIND>, optin)) return ELQ_ERR_CUDA;
+    if (!mma_args<KIND_I8>(p, 1, a) || !mma_optin(k_split, optin)) return ELQ_ERR_CUDA;
     const int stage = kABytes + bn * kStepBytes, hdr = 512 + 1024;
     const int steps = (int)((a.Kb + kStepBytes - 1) / kStepBytes), share = (steps + split - 1) / split;
     a.bn = bn;
     a.split = split;
     a.stages = std::min({kMmaStagesMax, (kMmaSmemMax - hdr) / stage, share});
     const int64_t tiles = (p.M + bn - 1) / bn * (((int64_t)p.N + kTileCh - 1) / kTileCh);
-    return status_of(launch(k_split<KIND>, dim3((unsigned)(tiles * split)), kMmaThreads, kMmaSmemMax, s, a, true, split));
+    return status_of(launch(k_split, dim3((unsigned)(tiles * split)), kMmaThreads, kMmaSmemMax, s, a, true, split));
 }
 
 // Pairs of CTAs where their tiles (an expert with rows has one at least) fill the
@@ -411,10 +410,10 @@ elq_status launch_split(const Product& p, int split, int bn, cudaStream_t s) {
 // 1792 x 4096: 16.7 against 18.2).
 template <int KIND>
 elq_status launch_mma(const Product& p, cudaStream_t s) {
-    if (!p.offsets) {
+    if constexpr (KIND == KIND_I8) {        // dense products are of codes
         int bn = 0;
-        const int split = split_plan(p, KIND == KIND_I8 ? 1 : 2, &bn);
-        if (split > 1) return launch_split<KIND>(p, split, bn, s);
+        const int split = p.offsets ? 1 : split_plan(p, &bn);
+        if (split > 1) return launch_split(p, split, bn, s);
     }
     const int64_t pairs = ((int64_t)p.N + 2 * kTileCh - 1) / (2 * kTileCh);
     const int64_t row_tiles = std::max<int64_t>(std::min(p.E, p.M), (p.M + 255) / 256);
@@ -427,7 +426,7 @@ elq_status launch_mma(const Product& p, cudaStream_t s) {
 // against 5.2 split over K; 512 -> 512, six rows: 1.9 against 3.1).
 bool few_rows(const Product& p) {
     if (p.offsets || p.M <= 4) return p.M <= 8;
-    return p.M <= 8 && (int64_t)p.N * p.K * (p.kind == KIND_I8 ? 1 : 2) <= 1 << 18;
+    return p.M <= 8 && (int64_t)p.N * p.K <= 1 << 18;
 }
 
 elq_status run_product(const Product& p, cudaStream_t s) {

@@ -608,14 +608,13 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_mma(const __grid_constant__ 
 
 // ---- split over K ------------------------------------------------------------------
 //
-// A dense product with few tiles would leave most SMs idle and run each tile's K
+// A dense product (they are of codes) with few tiles would leave most SMs idle and run each tile's K
 // steps one after another.  Here a cluster of up to eight CTAs works on one tile,
 // each on its share of the K steps; the partial accumulators go to shared memory
 // and every CTA adds up and writes its share of the rows, reading the others'
 // partials through distributed shared memory in rank order (so the result does
 // not depend on timing).  Bound by latency: launch, one memory round trip, the
 // steps of a share, one exchange.
-template <int KIND>
 __global__ void __launch_bounds__(kMmaThreads, 1) k_split(const __grid_constant__ MmaArgs a) {
     extern __shared__ uint8_t smem[];
     uint64_t* full = reinterpret_cast<uint64_t*>(smem);
@@ -661,7 +660,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_split(const __grid_constant_
                 if (a.stall == 1 && blockIdx.x == 0 && k == k1 - 1) break;
                 if (!bar_wait(empty + st, ph ^ 1, abort_v, a.wait_ns)) break;
                 const uint32_t p = tiles0 + st * stage_bytes, fb = smem_addr(full + st);
-                const int c = k * (KIND == KIND_I8 ? kStepBytes : kStepBytes / 2);
+                const int c = k * kStepBytes;
                 mbar_arrive_expect_tx(full + st, kABytes + boxes * kBoxBytes);
                 copy_3d<1>(p, &a.tw, c, ch0, 0, fb);
                 for (int b = 0; b < boxes; ++b) copy_2d<1>(p + kABytes + b * kBoxBytes, &a.tx, c, row0 + b * kBoxRows, fb);
@@ -686,9 +685,9 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_split(const __grid_constant_
                 const int parts = min(4, (a.Kb - k * kStepBytes + 31) / 32);
                 if (parts == 4) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) umma<KIND, 1>(tmem, ad + 2 * i, bd + 2 * i, idesc, k > k0 || i > 0);
+                    for (int i = 0; i < 4; ++i) umma<KIND_I8, 1>(tmem, ad + 2 * i, bd + 2 * i, idesc, k > k0 || i > 0);
                 } else {
-                    for (int i = 0; i < parts; ++i) umma<KIND, 1>(tmem, ad + 2 * i, bd + 2 * i, idesc, k > k0 || i > 0);
+                    for (int i = 0; i < parts; ++i) umma<KIND_I8, 1>(tmem, ad + 2 * i, bd + 2 * i, idesc, k > k0 || i > 0);
                 }
                 umma_commit<1>(empty + st);
                 if (++st == a.stages) {
@@ -725,21 +724,19 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_split(const __grid_constant_
     // this CTA's rows: a warp one row, a lane four channels
     const int r0 = rows * rank / S, r1 = rows * (rank + 1) / S, ch = ch0 + 4 * lane;
     float sw[4] = {1.0f, 1.0f, 1.0f, 1.0f}, bias[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (KIND == KIND_I8) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (ch + j < a.N) {
-                sw[j] = __ldg(a.sw + ch + j);
-                if (a.bias) bias[j] = __ldg(a.bias + ch + j);
-            }
-    }
+    for (int j = 0; j < 4; ++j)
+        if (ch + j < a.N) {
+            sw[j] = __ldg(a.sw + ch + j);
+            if (a.bias) bias[j] = __ldg(a.bias + ch + j);
+        }
     const bool quad = a.ldy % 4 == 0 && ch + 4 <= a.N;
     for (int r = r0 + warp; r < r1; r += kMmaThreads / 32) {
         const uint32_t mine = smem_addr(part) + (r * kTileCh + 4 * lane) * 4;
         uint4 w[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            w[i] = make_uint4(0, 0, 0, 0);      // for codes a zero; fp32 partials past S are not added
+            w[i] = make_uint4(0, 0, 0, 0);
             if (i < S) {
                 uint32_t at;
                 asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(mine), "r"(i));
@@ -750,34 +747,19 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_split(const __grid_constant_
             }
         }
         float v[4];
-        if (KIND == KIND_I8) {
-            int t[4] = {0, 0, 0, 0};
+        int t[4] = {0, 0, 0, 0};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                t[0] += (int)w[i].x;
-                t[1] += (int)w[i].y;
-                t[2] += (int)w[i].z;
-                t[3] += (int)w[i].w;
-            }
-            const float sx = __ldg(a.sx + row0 + r);
+        for (int i = 0; i < 8; ++i) {
+            t[0] += (int)w[i].x;
+            t[1] += (int)w[i].y;
+            t[2] += (int)w[i].z;
+            t[3] += (int)w[i].w;
+        }
+        const float sx = __ldg(a.sx + row0 + r);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                v[j] = __fmul_rn(__fmul_rn((float)t[j], sx), sw[j]);
-                if (a.bias) v[j] = __fadd_rn(v[j], bias[j]);
-            }
-        } else {
-            v[0] = __uint_as_float(w[0].x);
-            v[1] = __uint_as_float(w[0].y);
-            v[2] = __uint_as_float(w[0].z);
-            v[3] = __uint_as_float(w[0].w);
-#pragma unroll
-            for (int i = 1; i < 8; ++i) {
-                if (i >= S) continue;
-                v[0] = __fadd_rn(v[0], __uint_as_float(w[i].x));
-                v[1] = __fadd_rn(v[1], __uint_as_float(w[i].y));
-                v[2] = __fadd_rn(v[2], __uint_as_float(w[i].z));
-                v[3] = __fadd_rn(v[3], __uint_as_float(w[i].w));
-            }
+        for (int j = 0; j < 4; ++j) {
+            v[j] = __fmul_rn(__fmul_rn((float)t[j], sx), sw[j]);
+            if (a.bias) v[j] = __fadd_rn(v[j], bias[j]);
         }
         const int64_t at = (int64_t)(row0 + r) * a.ldy + ch;
         if (quad) {
