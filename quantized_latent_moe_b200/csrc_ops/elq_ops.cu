@@ -156,16 +156,22 @@ cudaError_t launch_rows_t(const RowArgs& a, int threads, cudaStream_t s) {
     return launch(k_rows<OP, VPT, VEC>, dim3((unsigned)std::min<int64_t>(a.rows, most)), threads, 0, s, a, false);
 }
 
-// k_rows: chunks of a row in registers, as few a thread as 512 threads allow,
-// or none for rows past 16384 values.
+// k_rows: chunks of a row in registers, as few a thread as 512 threads allow, or none (every step
+// reads its inputs again) for rows past 16384 values.  Aligned rows come here where k_pipe does not
+// take them (from 12289 values on, fp32 residual norms with a gate a row from 10241).  Of those the
+// quantiser and the plain norm read again, with half the registers and more warps an SM (2048 x
+// 14336 bf16: 39 and 42 us, 54 and 62 from registers); SwiGLU and the residual norm, which would do
+// their arithmetic again too, keep them (73 us, 103 read again; 1024 rows 59 us, 86).
 template <int OP, bool VEC>
 cudaError_t launch_rows_v(const RowArgs& a, cudaStream_t s) {
     const int chunks = (a.cols + 7) / 8;
     const int vpt = chunks <= kRowThreads ? 1 : chunks <= 2 * kRowThreads ? 2 : chunks <= 4 * kRowThreads ? 4 : 0;
     const int threads = vpt == 0 ? kRowThreads : std::max(32, ((chunks + vpt - 1) / vpt + 31) / 32 * 32);
-    if constexpr (OP == ROW_COMBINE || !VEC) {      // aligned rows of the others go through k_pipe
+    if constexpr (OP == ROW_COMBINE || !VEC) {      // aligned rows of the others, this short, go through k_pipe
         if (vpt == 1) return launch_rows_t<OP, 1, VEC>(a, threads, s);
         if (vpt == 2) return launch_rows_t<OP, 2, VEC>(a, threads, s);
+    }
+    if constexpr (!VEC || (OP != ROW_QUANT && OP != ROW_RMS)) {
         if (vpt == 4) return launch_rows_t<OP, 4, VEC>(a, threads, s);
     }
     return launch_rows_t<OP, 0, VEC>(a, kRowThreads, s);

@@ -341,6 +341,35 @@ def test_residual_norm_in_place(O):
         assert b.data_ptr() == H.data_ptr() and torch.equal(a, b) and torch.equal(n, m)
 
 
+@pytest.mark.parametrize("T", [2, 310])
+def test_wide_aligned_rows(O, T):
+    """Aligned rows longer than the ring in shared memory takes: 14336 values, and fp32 rows of 10248 with a gate a row."""
+    g, C = rng(T), 14336
+    v = randn(g, T, C, dtype=torch.bfloat16)
+    r, (q, s) = O.quantize_i8(v), codes64(v)
+    assert torch.equal(r.scale, s) and torch.equal(r.q.double(), q)
+    w = randn(g, C)
+    ref = rms64(v, w, 1e-6)
+    check(O.rms_norm(v, w), ref, NORM * ref.abs(), torch.bfloat16)
+    gu = randn(g, T, 2 * C, dtype=torch.bfloat16)
+    a, b = gu[:, :C].double(), gu[:, C:].double()
+    ref = a * torch.sigmoid(a) * b
+    check_codes(O.swiglu_i8(gu), ref, 5 * U32 * (1 + 2.0 ** -16) * ref.abs() + 2.0 ** -119 * b.abs())
+    for H, Y, G in ((randn(g, T, C, dtype=torch.bfloat16), v, randn(g, C)), (randn(g, T, 10248), randn(g, T, 10248), randn(g, T, 10248))):
+        post, pre = randn(g, H.shape[1]), randn(g, H.shape[1])
+        want = O.residual_norm(H, Y, post, gate=G, next_weight=pre, next_dtype=torch.float32)
+        n = rms64(Y, post, 1e-6) * G.double()
+        ref = H.double() + n
+        err = NORM * n.abs() + 2 * U32 * (H.double().abs() + n.abs())
+        check(want[0], ref, err, H.dtype)
+        f = (err.square().sum(-1, keepdim=True) / ref.square().sum(-1, keepdim=True)).sqrt()
+        rstd = 1 / torch.sqrt(ref.square().mean(-1, keepdim=True) + 1e-6)
+        ref2 = rms64(ref, pre, 1e-6)
+        check(want[1], ref2, (err * rstd * pre.double().abs() + (f + NORM) * ref2.abs()) * (1 + 2.0 ** -10), torch.float32)
+        got = O.residual_norm(H, Y, post, gate=G, next_weight=pre, next_dtype=torch.float32, out=H)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_vectors_off_sixteen_bytes(O):
     """Weights, gates, bias and scales that start on a 4-byte boundary only."""
     g = rng(31)
