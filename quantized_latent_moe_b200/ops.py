@@ -234,7 +234,12 @@ def residual_norm(h: torch.Tensor, y: torch.Tensor, post_weight: torch.Tensor | 
 
 def status(device=None, stream=None) -> int:
     """Blocking: whether a product's bounded device wait ran out since the last
-    call (0, or the timeout status)."""
+    call (0, or the timeout status), on the device of ``stream``, or on ``device``
+    (by default the current one, its current stream)."""
+    if stream is not None:
+        if device is not None and torch.cuda.device(device).idx != stream.device.index:
+            raise ElqError(-1, "status: stream of another device")
+        device = stream.device
     with torch.cuda.device(device):
         s = torch.cuda.current_stream() if stream is None else stream
         return int(lib().elq_ops_status(s.cuda_stream))

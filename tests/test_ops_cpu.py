@@ -184,6 +184,36 @@ def test_binding_is_rebuilt_for_another_torch_or_python(L, monkeypatch, tmp_path
     assert len(ran) == first + 1
 
 
+def test_status_reads_the_streams_device(monkeypatch):
+    """The error word is a device's: a stream's own, whatever the current device is."""
+    entered = []
+
+    class On:
+        def __init__(self, device):
+            self.idx = device if device is None or isinstance(device, int) else torch.device(device).index
+
+        def __enter__(self):
+            entered.append(self.idx)
+
+        def __exit__(self, *a):
+            pass
+
+    class Stream:
+        device, cuda_stream = torch.device("cuda", 3), 77
+
+    class Lib:
+        @staticmethod
+        def elq_ops_status(s):
+            return s
+
+    monkeypatch.setattr(torch.cuda, "device", On)
+    monkeypatch.setattr(ops, "lib", lambda: Lib)
+    assert ops.status(stream=Stream()) == 77 and entered == [3]
+    assert ops.status(3, stream=Stream()) == 77 and entered == [3, 3]
+    with pytest.raises(elq.ElqError):
+        ops.status(0, stream=Stream())
+
+
 def test_dequantize():
     r = ops.I8Rows(torch.tensor([[1, -2], [127, 0]], dtype=torch.int8), torch.tensor([0.5, 2.0]))
     assert torch.equal(r.dequantize(), torch.tensor([[0.5, -1.0], [254.0, 0.0]]))
