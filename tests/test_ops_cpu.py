@@ -173,6 +173,7 @@ def test_binding_is_rebuilt_for_another_torch_or_python(L, monkeypatch, tmp_path
     monkeypatch.setattr(build, "BINDING", str(made))
     monkeypatch.setattr(build, "BINDING_FOR", str(tmp_path / "_ops.for"), raising=False)
     monkeypatch.setattr(build, "_run", run)
+    monkeypatch.setattr(build, "deps", lambda: [build.LIB])     # the library is not this test's to build
     build.build()
     first = len(ran)
     build.build()
