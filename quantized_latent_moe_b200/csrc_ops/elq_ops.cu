@@ -117,7 +117,7 @@ bool launch_pipe(RowArgs a, cudaStream_t s, cudaError_t* e) {
                    (gate && a.gate_rows < a.rows ? 2 : 0);
     const size_t plane = (size_t)vpt * threads * 16;
     // Many rows with weights to share: several rows of a CTA at a time (2048 x 4096
-    // bf16, residual norm: 21.2 us with three, 27.9 with one; norm: 12.3 and 19.5).
+    // bf16, residual norm: 18.1 us with three, 22.8 with one; norm: 12.2 and 19.0).
     int groups = 1, d = 1;
     auto smem = [&](int g, int dd) { return (a.w_planes + (size_t)g * dd * a.row_planes) * plane; };
     if (many) {
@@ -131,7 +131,7 @@ bool launch_pipe(RowArgs a, cudaStream_t s, cudaError_t* e) {
     auto go = [&](auto v, auto dd) {
         constexpr int V = decltype(v)::value, D = decltype(dd)::value;
         if constexpr (OP == ROW_RESIDUAL) {
-            // one 16-bit type throughout is known at compile time (2048 x 4096 bf16: 21.2 us, 24.6 with
+            // one 16-bit type throughout is known at compile time (2048 x 4096 bf16: 18.1 us, 22.0 with
             // the types chosen as it runs); mixed types are not
             const bool same = a.x_type == a.h_type && a.n && a.n_type == a.h_type;
             if (same && a.x_type == ELQ_BF16) *e = launch_pipe_t<OP, V, D, ELQ_BF16>(a, threads, groups, smem(groups, d), s);

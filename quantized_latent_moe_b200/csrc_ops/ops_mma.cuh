@@ -18,9 +18,10 @@
 //
 // Bound by the weights' HBM traffic where groups are small, by L2 to shared memory
 // and the tensor cores (and power) where rows are many.  Measured on B200: 256 rows
-// over 128 experts of 2048 x 1792 codes 75 us (6.3 TB/s), 16384 rows 95 us (5.9
-// TB/s; bf16, 1792 x 1024: 96 us), dense 8192 x 4096 x 4096 codes 85 us (3.2 POP/s,
-// of 4.58 that MMAs alone reach).
+// over 128 experts of 2048 x 1792 codes 75 us (6.3 TB/s), 16384 rows 92 to 97 us
+// (5.8 TB/s; bf16, 1792 x 1024: 96 us), dense 8192 x 4096 x 4096 codes 87 us (3.2
+// POP/s, of 4.54 that MMAs alone reach), 2048 x 1792 x 4096 16.2 us: 9.5 us and 0.51
+// per 128 of K.
 #pragma once
 
 #include <cuda.h>
@@ -152,8 +153,8 @@ __device__ __forceinline__ void umma_commit(uint64_t* bar) {
 }
 // One lane of the warp.  Chosen by elect.sync, not by its number: the compiler then
 // knows that a single thread issues what follows, and keeps the MMAs' operands in
-// uniform registers (an MMA of 32 rows is issued every 21 ns; behind `lane == 0`
-// every 80 to 100, which bounded whole products).
+// uniform registers (a loop of MMAs of 32 rows issues one every 22 ns, behind
+// `lane == 0` every 32; 8192 x 4096 x 4096 codes: 87 us, 115 behind `lane == 0`).
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));

@@ -18,9 +18,10 @@
 //           for each, as do aligned rows where that is quicker.
 //
 // Measured on B200: 8192 x 4096 bf16 to codes 21 us (4.8 TB/s), 16384 gathered rows
-// of 1792 22.6, SwiGLU of 16384 x 2048 19.2 (4.4 TB/s), norm of 2048 x 4096 bf16 12,
-// residual norm with the next norm 18.5 (3.6 TB/s); one row of 4096 2 to 5 us.  For
-// many rows instruction issue is what keeps them from HBM speed.
+// of 1792 22.6, SwiGLU of 16384 x 2048 19.7 (4.3 TB/s), norm of 2048 x 4096 bf16 12,
+// residual norm with the next norm 18.1 (3.7 TB/s); one row of 4096 2.6 to 5 us.  What
+// keeps many rows from HBM speed is instruction issue for codes, and for the norms
+// latency: 12 warps an SM, two dependent reductions a row.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -456,7 +457,7 @@ __device__ __forceinline__ float row_rstd(Reduce& rr, float inv_cols, float eps,
 // reciprocal (2^-23), then its remainder added back once, which leaves 2^-45 beside the one
 // rounding.  So h is within 5 * 2^-24 of its value.  Where d passes 2^126 (g < -87.3) the
 // reciprocal is flushed and h is zero; the bound on -g keeps d finite there.  (By __fdiv_rn the
-// same values came at 28 us for 16384 x 2048, against 19.2.)
+// same values came at 28 us for 16384 x 2048, against 19.7.)
 __device__ __forceinline__ f32x2 swiglu2(f32x2 g, f32x2 u) {
     const float2 a = halves(g);
     const f32x2 z = pair(-a.x, -a.y);
