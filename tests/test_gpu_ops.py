@@ -873,6 +873,27 @@ def test_stream_argument_keeps_inputs(O):
     torch.cuda.synchronize()
 
 
+def test_stream_argument_in_a_capture(O):
+    """Calls that name the stream being captured, their intermediates dropped as they go, replay as eager calls."""
+    st, g = torch.cuda.Stream(), rng(10)
+    x, w = randn(g, 40, 512), O.quantize_i8(randn(g, 256, 512))
+    call = lambda: O.i8_matmul(O.rms_norm_i8(x, stream=st), w, stream=st)
+    call()
+    torch.cuda.synchronize()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr, stream=st):
+        y = call()
+        z = O.i8_matmul(O.quantize_i8(y, stream=st), O.I8Rows(w.q[:, :256], w.scale), stream=st)
+    x.mul_(-2)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        gr.replay()
+    torch.cuda.synchronize()
+    want = call()
+    torch.cuda.synchronize()
+    assert torch.equal(y, want) and torch.equal(z, O.i8_matmul(O.quantize_i8(want), O.I8Rows(w.q[:, :256], w.scale)))
+
+
 def test_out_counts_as_written_in_place(O):
     """A backward pass that saved what a call then writes raises, and does not use the new values."""
     h, y = torch.randn(4, 64, device="cuda"), torch.randn(4, 64, device="cuda")
